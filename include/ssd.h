@@ -78,7 +78,7 @@
 extern "C" {
 #endif
 
-#define SSD_ABI_VERSION 11
+#define SSD_ABI_VERSION 12
 
 typedef enum {
   SSD_OK = 0,
@@ -415,6 +415,107 @@ ssd_status ssd_gated_rmsnorm_bwd(const ssd_norm_problem* problem, const void* do
                                  const void* z, const float* weight, void* dy, void* dz,
                                  float* dweight, void* workspace, size_t workspace_bytes,
                                  void* stream);
+
+/*
+ * Gated delta rule: the linear recurrence whose update erases what the state holds
+ * along the key before it writes.  Per sequence and head h (group h / (nheads /
+ * ngroups)), with the state S of shape (headdim, dstate) and a_t = exp(g_t):
+ *
+ *     S_t = a_t S_{t-1} + beta_t (v_t - a_t S_{t-1} k_t) k_t^T
+ *     o_t = scale * S_t q_t,          S_{-1} = init,   final = S_last
+ *
+ * It stands beside the SSD scan with the scan's layouts (v for x, k for B, q for C):
+ *     v, out, dout, dv        (batch, seqlen, nheads, headdim)     io dtype
+ *     q, k, dq, dk            (batch, seqlen, ngroups, dstate)     io dtype
+ *     g, beta, dg, dbeta      (batch, seqlen, nheads)              fp32
+ *     init, final, d_final, d_init  (nstates, nheads, headdim, dstate)  fp32
+ *     cu_seqlens              (nseq + 1) int32, as for ssd_fwd
+ * and the conventions at the top of this file, with no second stream: every kernel of
+ * a call runs on `stream`.  A NULL stream is the current device's default stream.
+ *  - q and k are used as given.  The recurrence contracts where beta |k|^2 <= 2 and
+ *    g <= 0 (unit keys, beta in [0, 1]); nothing checks this.
+ *  - g below -256 counts as -256 (exp of it is zero in fp32): a gate of -inf resets the
+ *    state.  beta = 0 writes nothing; its own gradient is still the formula's.
+ *  - Chunked form (ssd_delta_fwd, ssd_delta_bwd): chunks of 64 tokens.  The states and
+ *    the gradients of g, beta and init are fp32 results of fp32 accuracy (operands of
+ *    the matrix products are split into two bf16 parts, three for fp32 io).  An
+ *    infinity or a NaN in an input can spread over its whole chunk, earlier tokens of
+ *    it included, and goes on through the states; later sequences are not touched.
+ *  - Tokens behind the last sequence of cu_seqlens are not computed: their rows of
+ *    every output stay as they were.
+ *  - Supported: io dtype f32 or bf16; headdim and dstate in {16, 32, 64, 128};
+ *    nheads % ngroups == 0; 64 * nheads * headdim * 4 and 64 * ngroups * dstate * 4 at
+ *    most 2^31 - 1; finite scale; any seqlen >= 0.
+ *  - flags: SSD_FLAG_SAVE_FOR_BWD (ssd_delta_fwd) and SSD_FLAG_FROM_SAVED
+ *    (ssd_delta_bwd), with the meaning they have for ssd_fwd and ssd_bwd; any other bit
+ *    is SSD_ERR_UNSUPPORTED.
+ */
+typedef struct {
+  int32_t batch, seqlen, nheads, headdim, dstate, ngroups;
+  int32_t nseq;      /* sequences when cu_seqlens is given, otherwise ignored */
+  int32_t io_dtype;  /* ssd_dtype of q, k, v, out and their gradients */
+  int32_t flags;
+  float scale;
+} ssd_delta_problem;
+
+/* Workspaces in bytes (0 for an invalid problem or one without tokens).  A
+ * SSD_FLAG_SAVE_FOR_BWD forward needs the backward's. */
+size_t ssd_delta_fwd_workspace_bytes(const ssd_delta_problem* problem, int32_t packed);
+size_t ssd_delta_bwd_workspace_bytes(const ssd_delta_problem* problem, int32_t packed);
+/* Forward.  init_states (NULL = 0) and final_states may be NULL. */
+ssd_status ssd_delta_fwd(const ssd_delta_problem* problem, const void* q, const void* k, const void* v,
+                         const float* g, const float* beta, const float* init_states,
+                         const int32_t* cu_seqlens, void* out, float* final_states,
+                         void* workspace, size_t workspace_bytes, void* stream);
+/* Backward for L = <dout, out> + <d_final_states, final>.  d_final_states (NULL = 0)
+ * and d_init_states may be NULL.  dq and dk are summed over each group's heads in fp32
+ * before rounding, in a fixed order. */
+ssd_status ssd_delta_bwd(const ssd_delta_problem* problem, const void* q, const void* k, const void* v,
+                         const float* g, const float* beta, const float* init_states,
+                         const int32_t* cu_seqlens, const void* dout, const float* d_final_states,
+                         void* dq, void* dk, void* dv, float* dg, float* dbeta, float* d_init_states,
+                         void* workspace, size_t workspace_bytes, void* stream);
+/* Recurrent form, for decoding: the seqlen tokens (one, or a few drafted ones) of each
+ * of `batch` sequences, on states held in a cache of nslots slots, states
+ * (nslots, nheads, headdim, dstate) fp32, updated in place in fp32 arithmetic.
+ * slots (batch) int32 names each sequence's slot; NULL: sequence b uses slot b (nslots
+ * must then be at least batch).  A sequence whose slot lies outside [0, nslots) is
+ * padding: its rows of out and every state stay as they were.  Where several sequences
+ * name one slot, the first of them runs and the others are padding.  problem->nseq and
+ * flags must be 0.  No workspace. */
+ssd_status ssd_delta_step(const ssd_delta_problem* problem, const void* q, const void* k, const void* v,
+                          const float* g, const float* beta, const int32_t* slots, int32_t nslots,
+                          float* states, void* out, void* stream);
+
+/*
+ * State cache: the fp32 states of `n` sequences, (n, nheads, headdim, dstate) as
+ * ssd_fwd's and ssd_delta_fwd's final and init states, parked in 8 bits in the slots of
+ * a cache (quantised as they are written) and read back.  One fp32 scale for each
+ * state row of dstate values:
+ *     codes (nslots, nheads, headdim, dstate) 8-bit,  scales (nslots, nheads, headdim)
+ *     SSD_CACHE_INT8: scale = max|x| / 127 rounded to fp32, code = x / scale rounded to
+ *                     nearest even; off by at most scale / 2 and the product's rounding
+ *     SSD_CACHE_E4M3: (1-4-3 floating point, largest value 448) scale = the smallest
+ *                     power of two >= 2^-126 with max|x| <= 448 scale, code = x / scale
+ *                     rounded to nearest even; off by at most 2^-4 |x| or 2^-10 scale
+ * and a value reads back as code * scale.  A row of zeros has scale 0; a row with an
+ * infinity or a NaN has scale NaN and reads back as NaN throughout.
+ * slots (n) int32 (NULL: sequence i uses slot i): a slot outside [0, nslots) is not
+ * written, and reads as a state of zeros; of several sequences that write one slot the
+ * first does.  States that go on being updated stay in fp32: a decode
+ * step's rounding to 8 bits would add up over the tokens.
+ * Supported: dstate in {16, 32, 64, 128}, n <= 65535, nslots >= 1,
+ * nheads * headdim < 2^24.
+ */
+typedef enum { SSD_CACHE_INT8 = 0, SSD_CACHE_E4M3 = 1 } ssd_cache_format;
+typedef struct {
+  int32_t n, nslots, nheads, headdim, dstate;
+  int32_t format;  /* ssd_cache_format */
+} ssd_cache_problem;
+ssd_status ssd_state_cache_write(const ssd_cache_problem* problem, const float* states, const int32_t* slots,
+                                 void* codes, float* scales, void* stream);
+ssd_status ssd_state_cache_read(const ssd_cache_problem* problem, const void* codes, const float* scales,
+                                const int32_t* slots, float* states, void* stream);
 
 /* Plain device-to-device copy kernel of `bytes` bytes (16-byte multiple), used to
  * calibrate hardware traffic counters against a kernel of known traffic. */

@@ -75,7 +75,7 @@ def build(verbose=False):
     """Compile every source and link libssd.so; returns its path."""
     os.makedirs(BUILD_DIR, exist_ok=True)
     write_table_include()
-    srcs = sorted(glob.glob(os.path.join(CSRC, "*.hip"))) + [os.path.join(CSRC, "api.cpp")]
+    srcs = sorted(glob.glob(os.path.join(CSRC, "*.hip"))) + sorted(glob.glob(os.path.join(CSRC, "api*.cpp")))
     with concurrent.futures.ThreadPoolExecutor(max_workers=min(8, os.cpu_count() or 1)) as ex:
         objs = list(ex.map(_compile, srcs))
     tmp = OUT + ".tmp"

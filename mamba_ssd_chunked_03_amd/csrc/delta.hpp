@@ -1,0 +1,217 @@
+// Shared pieces of the gated delta rule's kernels (k_delta_*.hip) and the host
+// side's description of one problem.
+//
+// Per sequence and head, with the state S (P x N), a_t = exp(g_t):
+//   S_t = a_t S_{t-1} + b_t (v_t - a_t S_{t-1} k_t) k_t^T,   o_t = scale S_t q_t.
+// In chunks of C = 64 tokens, with G the running sum of g inside the chunk,
+// D_ij = exp(G_i - G_j) and S the state entering the chunk (rows are tokens):
+//   M = strict lower part of (K K^T . D),  R = M (I + diag(b) M)^-1  (strictly lower),
+//   X = V - exp(G) K S^T,   Z = X - R (b X),   U = b Z,
+//   O = scale (exp(G) Q S^T + (Q K^T . D) U),   S' = exp(G_C) S + (exp(G_C - G) U)^T K.
+// (I + b M)^-1 = I - b R and (I + M b)^-1 = I - R b, so that R alone serves the
+// forward, the backward and the gradient of b, also where b is zero.
+//
+// Precision.  The states and the gates' gradients are fp32 results, and an error of
+// the state is carried through every later chunk.  Matrix products run on the bf16
+// MFMA with fp32 accumulation, each fp32 operand split into bf16 planes
+// (x = x0 + x1 [+ x2], each the rounding of what the ones before leave): two planes
+// where the inputs are bf16 (those are one exact plane), the products x0 y0 + x0 y1
+// + x1 y0 leaving about 2^-17 of a product; three planes and six products where the
+// inputs are fp32.  Two planes cost 2-3 matrix instructions a product and stay 2-3
+// times above the fp32 matrix cores' rate.
+#pragma once
+
+#include "internal.hpp"
+
+namespace ssd {
+
+constexpr int kDeltaChunk = 64;
+
+// Natural-log gates below this are taken as this: exp of it is zero in fp32, and
+// running sums of it stay finite (a gate of -inf resets the state).
+constexpr float kDeltaMinGate = -256.f;
+
+struct DeltaProb {
+  int32_t B, L, H, P, N, G;
+  int32_t nst;   // state slots: batch rows, or packed sequences
+  int32_t io;    // 0 fp32, 1 bf16
+  int32_t packed;
+  int32_t flags;
+  float scale;
+  int64_t nck;   // chunk slots of 64 tokens
+  ChunkMap map;
+};
+
+// Regions of the workspace (byte offsets, 256-byte aligned).
+struct DeltaLayout {
+  size_t tab, seq_off, gates, R, Pm, fwd_end;  // the forward's
+  size_t Rt, Pt, S, Z, dS, F, end;             // kept for the backward, and the backward's
+};
+
+// Per-problem pointers of the chunked kernels.
+struct DeltaArgs {
+  ChunkMap map;
+  int32_t H, G, P, N, L;
+  float scale;
+  const void *q, *k, *v;
+  const float *g, *beta, *init;
+  void* out;
+  float* final_states;
+  float* gates;                // (nck, H, 3, 64): running log2 decay (high, low part), beta
+  uint16_t *R, *Pm, *Rt, *Pt;  // plane-split chunk matrices in fragment order (null: not kept)
+  float *S, *Z;                // kept for the backward: states entering each chunk, Z
+  // backward
+  const void* dout;
+  const float* d_final;
+  float *dS, *F, *d_init;
+  void *dq, *dk, *dv;
+  float *dg, *dbeta;
+};
+
+hipError_t launch_delta_prep(const DeltaProb& p, const DeltaArgs& a, hipStream_t st);
+hipError_t launch_delta_fwd(const DeltaProb& p, const DeltaArgs& a, hipStream_t st);
+hipError_t launch_delta_bwd_chain(const DeltaProb& p, const DeltaArgs& a, hipStream_t st);
+hipError_t launch_delta_bwd_grads(const DeltaProb& p, const DeltaArgs& a, hipStream_t st);
+hipError_t launch_delta_step(const DeltaProb& p, const void* q, const void* k, const void* v, const float* g,
+                             const float* beta, const int32_t* slots, int nslots, float* states, void* out,
+                             hipStream_t st);
+hipError_t launch_state_cache(bool write, int n, int nslots, int H, int P, int N, int format, float* states,
+                              const int32_t* slots, void* codes, float* scales, hipStream_t st);
+
+// ------------------------------------------------------------- io types ----
+// PI: bf16 planes that hold an input exactly; PM: planes of a computed operand.
+struct IoBf16 {
+  using T = uint16_t;
+  static constexpr int PI = 1, PM = 2;
+};
+struct IoF32 {
+  using T = float;
+  static constexpr int PI = 3, PM = 3;
+};
+
+template <int NP>
+struct Planes {
+  bf16x8 p[NP];
+};
+
+// planes of 4 floats, 8 bytes each (consecutive elements)
+template <int NP>
+__device__ __forceinline__ void split4(f32x4 x, uint2 (&o)[NP]) {
+#pragma unroll
+  for (int i = 0; i < NP; ++i) {
+    o[i] = make_uint2(pack_bf2(x[0], x[1]), pack_bf2(x[2], x[3]));
+    if (i + 1 < NP) {
+      x[0] -= bf_lo(o[i].x);
+      x[1] -= bf_hi(o[i].x);
+      x[2] -= bf_lo(o[i].y);
+      x[3] -= bf_hi(o[i].y);
+    }
+  }
+}
+// planes of 8 floats
+template <int NP>
+__device__ __forceinline__ void split8(f32x4 a, f32x4 b, u32x4 (&o)[NP]) {
+  uint2 x[NP], y[NP];
+  split4<NP>(a, x);
+  split4<NP>(b, y);
+#pragma unroll
+  for (int i = 0; i < NP; ++i) o[i] = u32x4{x[i].x, x[i].y, y[i].x, y[i].y};
+}
+
+// c += sum of the products of planes i of a and j of b with i + j < PM, smallest first.
+template <int PM, int NA, int NB>
+__device__ __forceinline__ f32x4 mma(const Planes<NA>& a, const Planes<NB>& b, f32x4 c) {
+#pragma unroll
+  for (int s = PM - 1; s >= 0; --s)
+#pragma unroll
+    for (int i = 0; i < NA; ++i)
+      if (s - i >= 0 && s - i < NB) c = mfma_bf16(a.p[i], b.p[s - i], c);
+  return c;
+}
+
+// MFMA operand from LDS planes stored [row][k] (k contiguous, row stride ld elements):
+// lane (q, r) reads elements 8q..8q+7 of row r.  `t` points at [row0][k0] of plane 0.
+template <int NP>
+__device__ __forceinline__ Planes<NP> lds_rows(const uint16_t* t, int ld, int plane, int lane) {
+  Planes<NP> f;
+#pragma unroll
+  for (int i = 0; i < NP; ++i)
+    f.p[i] = as_bf16x8(*(const u32x4*)(t + i * plane + (lane & 15) * ld + 8 * (lane >> 4)));
+  return f;
+}
+// ... stored [k][row] (the contraction along the LDS rows), by transposing reads.
+template <int NP>
+__device__ __forceinline__ Planes<NP> lds_cols(const uint16_t* t, int ld, int plane, int lane) {
+  Planes<NP> f;
+#pragma unroll
+  for (int i = 0; i < NP; ++i) f.p[i] = frag_kmajor(t + i * plane, ld, lane);
+  return f;
+}
+
+// An io row's 8 elements as raw 16-byte pieces (one for bf16, two for fp32), loaded
+// through a range-checked resource, and their planes.
+template <class IO>
+struct Raw8;
+template <>
+struct Raw8<IoBf16> {
+  u32x4 v;
+  __device__ __forceinline__ void load(brsrc r, uint32_t off) { v = buf_load16(r, off); }
+  __device__ __forceinline__ void planes(u32x4 (&o)[1]) const { o[0] = v; }
+};
+template <>
+struct Raw8<IoF32> {
+  f32x4 a, b;
+  __device__ __forceinline__ void load(brsrc r, uint32_t off) {
+    a = __builtin_bit_cast(f32x4, buf_load16(r, off));
+    b = __builtin_bit_cast(f32x4, buf_load16(r, off + 16));
+  }
+  __device__ __forceinline__ void planes(u32x4 (&o)[3]) const { split8<3>(a, b, o); }
+};
+template <class IO>
+__device__ __forceinline__ Planes<IO::PI> raw_planes(const Raw8<IO>& x) {
+  u32x4 o[IO::PI];
+  x.planes(o);
+  Planes<IO::PI> f;
+#pragma unroll
+  for (int i = 0; i < IO::PI; ++i) f.p[i] = as_bf16x8(o[i]);
+  return f;
+}
+
+// 4 consecutive io elements <-> fp32
+__device__ __forceinline__ f32x4 load4(brsrc r, uint32_t off, IoBf16) {
+  typedef int i32x2 __attribute__((ext_vector_type(2)));
+  const i32x2 w = __builtin_bit_cast(i32x2, __builtin_amdgcn_raw_buffer_load_b64(r, off, 0, 0));
+  return f32x4{bf_lo(w[0]), bf_hi(w[0]), bf_lo(w[1]), bf_hi(w[1])};
+}
+__device__ __forceinline__ f32x4 load4(brsrc r, uint32_t off, IoF32) {
+  return __builtin_bit_cast(f32x4, buf_load16(r, off));
+}
+__device__ __forceinline__ void store4io(brsrc r, uint32_t off, f32x4 v, IoBf16) {
+  typedef uint32_t u32x2v __attribute__((ext_vector_type(2)));
+  const u32x2v w = {pack_bf2(v[0], v[1]), pack_bf2(v[2], v[3])};
+  __builtin_amdgcn_raw_buffer_store_b64(w, r, off, 0, 0);
+}
+__device__ __forceinline__ void store4io(brsrc r, uint32_t off, f32x4 v, IoF32) {
+  buf_store16(r, off, __builtin_bit_cast(u32x4, v));
+}
+
+// 2^(h + l) of a high and a small low part (their sum in fp32 would drop the low one)
+__device__ __forceinline__ float exp2_hl(float h, float l) {
+  const float e = exp2_fast(h);
+  return fmaf(e, l * 0.6931471805599453f, e);
+}
+
+// A buffer offset that no resource covers (loads zero, stores nothing).
+constexpr uint32_t kNoOffset = 0x80000000u;
+
+// ------------------------------------------------- chunk matrices, stored ----
+// R and P (64 x 64, lower triangular) and their transposes (upper triangular) are kept
+// as the six 16 x 32 blocks that are not all zero, 1 KB a block and plane in the order
+// of an MFMA operand load (lane (q, r): columns 8q..8q+7 of row r).  Row block R of a
+// lower matrix needs column block 0, and 1 from R = 2 on; of a transposed one column
+// block 1, and 0 up to R = 1.
+constexpr int kTriBlocks = 6, kTriPlane = kTriBlocks * 512;  // elements of one plane
+__host__ __device__ __forceinline__ int tri_block(int R, int S) { return R < 2 ? R : 2 * (R - 1) + S; }
+__host__ __device__ __forceinline__ int trit_block(int R, int S) { return R < 2 ? 2 * R + S : R + 2; }
+
+}  // namespace ssd

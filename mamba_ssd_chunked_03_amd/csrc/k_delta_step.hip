@@ -1,0 +1,131 @@
+// Gated delta rule, recurrent form: T >= 1 tokens of each sequence of a decode batch,
+// on states that stay in place in a slotted cache (fp32).
+//
+//   a = exp(g), r = v - a (S k), u = b r, S <- a S + u k^T, o = scale S q,
+// with o evaluated as scale (a (S q) + u (k . q)), so that S k and S q are reduced
+// together, before the update.  State rows (headdim) do not interact: a workgroup
+// takes some rows of one (sequence, head), N / 4 lanes a row with 4 elements each, and
+// holds them in registers over the T tokens.
+//
+// Bound: the states' bytes, read once and written once (8 bytes an element).
+//
+// A sequence whose slot is out of range is padding: nothing of it is read or written.
+// Of several sequences that name one slot the first runs and the others are treated
+// as padding: running them together would race on the state.
+#include "delta.hpp"
+
+namespace ssd {
+
+// Sum over the LPR = N / 4 lanes of a row, 4 | 8 | 16 | 32 consecutive lanes.
+template <int LPR>
+__device__ __forceinline__ float row_total(float v) {
+  if constexpr (LPR >= 16) {
+    v = row_sum16(v);
+    if constexpr (LPR == 32) {
+      const auto a = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+      v = __uint_as_float(a[0]) + __uint_as_float(a[1]);
+    }
+  } else {
+    v += dpp_f<kQuadXor1>(0.f, v);
+    v += dpp_f<kQuadXor2>(0.f, v);
+    if constexpr (LPR == 8) v += dpp_f<kRowHalfMirror>(0.f, v);
+  }
+  return v;
+}
+
+__device__ __forceinline__ f32x4 io4(const uint16_t* p) {
+  const uint2 w = *(const uint2*)p;
+  return f32x4{bf_lo(w.x), bf_hi(w.x), bf_lo(w.y), bf_hi(w.y)};
+}
+__device__ __forceinline__ f32x4 io4(const float* p) { return *(const f32x4*)p; }
+__device__ __forceinline__ float io1(const uint16_t* p) { return bf2f(*p); }
+__device__ __forceinline__ float io1(const float* p) { return *p; }
+__device__ __forceinline__ void put1(uint16_t* p, float v) { *p = f2bf(v); }
+__device__ __forceinline__ void put1(float* p, float v) { *p = v; }
+__device__ __forceinline__ float dot4(f32x4 a, f32x4 b) {
+  return a[0] * b[0] + a[1] * b[1] + a[2] * b[2] + a[3] * b[3];
+}
+
+// Whether sequence b runs: its slot lies in [0, nslots) and no earlier sequence names it.
+__device__ __forceinline__ bool slot_runs(const int32_t* slots, int b, int slot, int nslots) {
+  int dup = 0;
+  for (int i = threadIdx.x; i < b; i += blockDim.x) dup |= slots[i] == slot;
+  return !__syncthreads_or(dup) && slot >= 0 && slot < nslots;
+}
+
+template <int N, class IO, int RPT>
+__global__ __launch_bounds__(256) void delta_step_kernel(int T, int H, int G, int P, float scale,
+                                                         const typename IO::T* __restrict__ Q,
+                                                         const typename IO::T* __restrict__ K,
+                                                         const typename IO::T* __restrict__ V,
+                                                         const float* __restrict__ g, const float* __restrict__ beta,
+                                                         const int32_t* __restrict__ slots, int nslots,
+                                                         float* __restrict__ states, typename IO::T* __restrict__ out) {
+  constexpr int LPR = N / 4, RP = 256 / LPR;  // lanes a row, rows a pass
+  const int blocks = (P + RP * RPT - 1) / (RP * RPT);
+  const int rb = blockIdx.x % blocks, h = (int)((blockIdx.x / blocks) % H), b = (int)(blockIdx.x / blocks / H);
+  const int lr = threadIdx.x / LPR, n0 = (threadIdx.x % LPR) * 4;
+  const int slot = slots ? slots[b] : b;
+  if (slots) {
+    if (!slot_runs(slots, b, slot, nslots)) return;  // (the same for the whole workgroup)
+  }
+  float* S = states + ((int64_t)slot * H + h) * P * N;
+  f32x4 s[RPT];
+  int p[RPT];
+#pragma unroll
+  for (int i = 0; i < RPT; ++i) {
+    p[i] = rb * RP * RPT + i * RP + lr;
+    s[i] = p[i] < P ? *(const f32x4*)(S + (int64_t)p[i] * N + n0) : f32x4{0.f, 0.f, 0.f, 0.f};
+  }
+  const int grp = h / (H / G);
+  for (int t = 0; t < T; ++t) {
+    const int64_t tok = (int64_t)b * T + t;
+    const f32x4 k = io4(K + (tok * G + grp) * N + n0), q = io4(Q + (tok * G + grp) * N + n0);
+    const float a = expf(fmaxf(g[tok * H + h], kDeltaMinGate)), bt = beta[tok * H + h];
+    const float kq = row_total<LPR>(dot4(k, q));
+#pragma unroll
+    for (int i = 0; i < RPT; ++i) {
+      const float v = p[i] < P ? io1(V + (tok * H + h) * P + p[i]) : 0.f;
+      const float sk = row_total<LPR>(dot4(s[i], k)), sq = row_total<LPR>(dot4(s[i], q));
+      const float u = bt * (v - a * sk);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) s[i][e] = a * s[i][e] + u * k[e];
+      if (n0 == 0 && p[i] < P) put1(out + (tok * H + h) * P + p[i], scale * (a * sq + u * kq));
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < RPT; ++i)
+    if (p[i] < P) *(f32x4*)(S + (int64_t)p[i] * N + n0) = s[i];
+}
+
+template <int N, class IO>
+static void step_go(const DeltaProb& p, const void* q, const void* k, const void* v, const float* g,
+                    const float* beta, const int32_t* slots, int nslots, float* states, void* out, hipStream_t st) {
+  constexpr int RPT = 2, RP = 256 / (N / 4);
+  const int64_t wgs = (int64_t)p.B * p.H * ((p.P + RP * RPT - 1) / (RP * RPT));
+  using T = typename IO::T;
+  hipLaunchKernelGGL((delta_step_kernel<N, IO, RPT>), dim3((unsigned)wgs), dim3(256), 0, st, p.L, p.H, p.G, p.P,
+                     p.scale, (const T*)q, (const T*)k, (const T*)v, g, beta, slots, nslots, states, (T*)out);
+}
+
+hipError_t launch_delta_step(const DeltaProb& p, const void* q, const void* k, const void* v, const float* g,
+                             const float* beta, const int32_t* slots, int nslots, float* states, void* out,
+                             hipStream_t st) {
+  if (p.B == 0 || p.L == 0) return hipSuccess;
+  auto go = [&](auto io) {
+    using IO = decltype(io);
+    switch (p.N) {
+      case 16: step_go<16, IO>(p, q, k, v, g, beta, slots, nslots, states, out, st); break;
+      case 32: step_go<32, IO>(p, q, k, v, g, beta, slots, nslots, states, out, st); break;
+      case 64: step_go<64, IO>(p, q, k, v, g, beta, slots, nslots, states, out, st); break;
+      default: step_go<128, IO>(p, q, k, v, g, beta, slots, nslots, states, out, st); break;
+    }
+  };
+  if (p.io)
+    go(IoBf16{});
+  else
+    go(IoF32{});
+  return hipGetLastError();
+}
+
+}  // namespace ssd

@@ -28,6 +28,17 @@ class NormProblem(ctypes.Structure):
                 ("io_dtype", ctypes.c_int32), ("eps", ctypes.c_float)]
 
 
+class DeltaProblem(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in
+                ("batch", "seqlen", "nheads", "headdim", "dstate", "ngroups", "nseq", "io_dtype",
+                 "flags")] + [("scale", ctypes.c_float)]
+
+
+class CacheProblem(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in
+                ("n", "nslots", "nheads", "headdim", "dstate", "format")]
+
+
 FLAG_SAVE_FOR_BWD, FLAG_FROM_SAVED, FLAG_ONE_STREAM, FLAG_SEQUENTIAL_SCAN, FLAG_CHAINED_FWD = \
     1, 2, 4, 8, 16
 FLAG_BWD_FUSED = 32
@@ -88,10 +99,17 @@ _SIGS = {
     "ssd_gated_rmsnorm_bwd_workspace_bytes": ([_P], _SZ),
     "ssd_gated_rmsnorm_fwd": ([_P] + [_P] * 5 + [_P], _I32),
     "ssd_gated_rmsnorm_bwd": ([_P] + [_P] * 8 + [_SZ, _P], _I32),
+    "ssd_delta_fwd_workspace_bytes": ([_P, _I32], _SZ),
+    "ssd_delta_bwd_workspace_bytes": ([_P, _I32], _SZ),
+    "ssd_delta_fwd": ([_P] + [_P] * 10 + [_SZ, _P], _I32),
+    "ssd_delta_bwd": ([_P] + [_P] * 16 + [_SZ, _P], _I32),
+    "ssd_delta_step": ([_P] + [_P] * 6 + [_I32, _P, _P, _P], _I32),
+    "ssd_state_cache_write": ([_P] + [_P] * 5, _I32),
+    "ssd_state_cache_read": ([_P] + [_P] * 5, _I32),
 }
 EXPORTS = tuple(_SIGS)
 # The argument lists above follow this version of include/ssd.h (SSD_ABI_VERSION).
-ABI_VERSION = 11
+ABI_VERSION = 12
 
 _lib = None
 
@@ -554,3 +572,229 @@ def gated_rmsnorm_bwd(dout, y, z, weight, group, eps=1e-5, workspace=None, grads
         return launch, grads
     launch()
     return grads
+
+
+# ------------------------------------------------------- gated delta rule ----
+_IO = {torch.float32: F32, torch.bfloat16: BF16}
+
+
+def _delta_check(q, k, v, g, beta, init, cu_seqlens):
+    """Shapes and dtypes of the chunked delta rule's inputs: (batch, seqlen, nheads, headdim,
+    ngroups, dstate, state count, io dtype), as _dims gives them for (v, k)."""
+    if not isinstance(v, torch.Tensor) or v.dim() != 4:
+        raise ValueError("v must be a 4-D tensor (batch, seqlen, nheads, headdim)")
+    if not isinstance(k, torch.Tensor) or k.dim() != 4:
+        raise ValueError("k must be a 4-D tensor (batch, seqlen, ngroups, dstate)")
+    if v.dtype not in _IO:
+        raise ValueError("v must be float32 or bfloat16")
+    batch, seqlen, H, P = v.shape
+    G, N = k.shape[2], k.shape[3]
+    _expect(k, "k", (batch, seqlen, G, N), v.dtype)
+    _expect(q, "q", (batch, seqlen, G, N), v.dtype)
+    _expect(g, "g", (batch, seqlen, H), torch.float32)
+    _expect(beta, "beta", (batch, seqlen, H), torch.float32)
+    nst = batch
+    if cu_seqlens is not None:
+        if not isinstance(cu_seqlens, torch.Tensor) or cu_seqlens.dim() != 1 or cu_seqlens.numel() < 1:
+            raise ValueError("cu_seqlens must be a 1-D tensor of nseq + 1 offsets")
+        if cu_seqlens.dtype != torch.int32:
+            raise ValueError("cu_seqlens must be int32")
+        if batch != 1:
+            raise ValueError("packed sequences (cu_seqlens) must come in one batch row")
+        nst = cu_seqlens.numel() - 1
+    _expect(init, "init", (nst, H, P, N), torch.float32, required=False)
+    return batch, seqlen, H, P, G, N, nst, v.dtype
+
+
+def _delta_problem(dims, packed, scale, flags=0):
+    batch, seqlen, H, P, G, N, nst, io = dims
+    return DeltaProblem(batch, seqlen, H, P, N, G, nst if packed else 0, _IO[io], flags,
+                        N ** -0.5 if scale is None else float(scale))
+
+
+def _launcher(fn, args, dev, keep):
+    """launch(): the call, with `dev` current (a NULL stream is the current device's)."""
+    def launch():
+        with torch.cuda.device(dev):
+            _check(fn(*args), keep)
+    return launch
+
+
+def delta_workspace_bytes(k, v, cu_seqlens=None, backward=False):
+    """Workspace of delta_fwd (backward=False), or of delta_bwd and a saving delta_fwd, for
+    inputs shaped like k and v."""
+    if not (isinstance(k, torch.Tensor) and isinstance(v, torch.Tensor) and k.dim() == 4 and v.dim() == 4):
+        raise ValueError("k and v must be 4-D tensors")
+    if v.dtype not in _IO:
+        raise ValueError("v must be float32 or bfloat16")
+    packed = cu_seqlens is not None
+    nst = cu_seqlens.numel() - 1 if packed else v.shape[0]
+    prob = _delta_problem(tuple(v.shape) + (k.shape[2], k.shape[3], nst, v.dtype), packed, 1.0)
+    fn = lib().ssd_delta_bwd_workspace_bytes if backward else lib().ssd_delta_fwd_workspace_bytes
+    return fn(ctypes.byref(prob), int(packed))
+
+
+def delta_fwd(q, k, v, g, beta, scale=None, init=None, cu_seqlens=None, workspace=None, out=None,
+              final=None, save_for_backward=False, prepare=False):
+    """out, final_states of the gated delta rule in its chunked form (include/ssd.h):
+        S <- exp(g_t) S,  S <- S + beta_t (v_t - S k_t) k_t^T,  out_t = scale S q_t.
+    q, k (batch, seqlen, ngroups, dstate) and v (batch, seqlen, nheads, headdim) in one io
+    dtype (float32 or bfloat16); g, beta (batch, seqlen, nheads) float32.  scale defaults to
+    dstate ** -0.5.  init, cu_seqlens, workspace, out, final, save_for_backward and prepare as
+    for fwd."""
+    dims = _delta_check(q, k, v, g, beta, init, cu_seqlens)
+    batch, seqlen, H, P, G, N, nst, io = dims
+    _expect(out, "out", v.shape, io, required=False)
+    _expect(final, "final", (nst, H, P, N), torch.float32, required=False)
+    _expect(workspace, "workspace", (workspace.numel(),) if workspace is not None else (0,),
+            torch.uint8, required=False)
+    dev = _dev(q, k, v, g, beta, init, cu_seqlens, workspace, out, final)
+    packed = cu_seqlens is not None
+    prob = _delta_problem(dims, packed, scale, FLAG_SAVE_FOR_BWD if save_for_backward else 0)
+    L = lib()
+    if workspace is None:
+        need = L.ssd_delta_bwd_workspace_bytes if save_for_backward else L.ssd_delta_fwd_workspace_bytes
+        workspace = _ws(need(ctypes.byref(prob), int(packed)), dev)
+    if out is None:
+        out = torch.empty_like(v)
+    if final is None:
+        final = torch.empty(nst, H, P, N, dtype=torch.float32, device=dev)
+    args = (ctypes.byref(prob), _ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(beta), _ptr(init), _ptr(cu_seqlens),
+            _ptr(out), _ptr(final), _ptr(workspace), workspace.numel(), _stream(dev))
+    launch = _launcher(L.ssd_delta_fwd, args, dev, (prob, workspace))
+    if prepare:
+        return launch, out, final
+    launch()
+    return out, final
+
+
+def delta_bwd(q, k, v, g, beta, dout, scale=None, init=None, d_final=None, cu_seqlens=None,
+              workspace=None, from_saved=False, grads=None, prepare=False):
+    """Gradients of <dout, out> + <d_final, final> for delta_fwd: a dict with dq, dk, dv, dg,
+    dbeta and d_init (None without init).  d_final, workspace, from_saved, grads and prepare as
+    for bwd."""
+    dims = _delta_check(q, k, v, g, beta, init, cu_seqlens)
+    batch, seqlen, H, P, G, N, nst, io = dims
+    _expect(dout, "dout", v.shape, io)
+    _expect(d_final, "d_final", (nst, H, P, N), torch.float32, required=False)
+    _expect(workspace, "workspace", (workspace.numel(),) if workspace is not None else (0,),
+            torch.uint8, required=False)
+    if grads is not None:
+        for n, like in (("dq", q), ("dk", k), ("dv", v), ("dg", g), ("dbeta", beta)):
+            _expect(grads.get(n), "grads['%s']" % n, like.shape, like.dtype)
+        _expect(grads.get("d_init"), "grads['d_init']", (nst, H, P, N), torch.float32, required=init is not None)
+        if init is None and grads.get("d_init") is not None:
+            raise ValueError("grads['d_init'] must be given exactly when init is")
+    if from_saved and workspace is None:
+        raise ValueError("from_saved needs the forward's workspace")
+    dev = _dev(q, k, v, g, beta, dout, init, d_final, cu_seqlens, workspace,
+               *([] if grads is None else [t for t in grads.values() if t is not None]))
+    packed = cu_seqlens is not None
+    prob = _delta_problem(dims, packed, scale, FLAG_FROM_SAVED if from_saved else 0)
+    L = lib()
+    if workspace is None:
+        workspace = _ws(L.ssd_delta_bwd_workspace_bytes(ctypes.byref(prob), int(packed)), dev)
+    d = grads if grads is not None else {
+        "dq": torch.empty_like(q), "dk": torch.empty_like(k), "dv": torch.empty_like(v),
+        "dg": torch.empty_like(g), "dbeta": torch.empty_like(beta),
+        "d_init": None if init is None else torch.empty_like(init)}
+    args = (ctypes.byref(prob), _ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(beta), _ptr(init), _ptr(cu_seqlens),
+            _ptr(dout), _ptr(d_final), _ptr(d["dq"]), _ptr(d["dk"]), _ptr(d["dv"]), _ptr(d["dg"]),
+            _ptr(d["dbeta"]), _ptr(d.get("d_init")), _ptr(workspace), workspace.numel(), _stream(dev))
+    launch = _launcher(L.ssd_delta_bwd, args, dev, (prob, workspace))
+    if prepare:
+        return launch, d
+    launch()
+    return d
+
+
+def _check_slots(slots, n, nslots):
+    if n > 0 and nslots == 0:
+        raise ValueError("the cache must hold at least one slot")
+    if slots is None:
+        if nslots < n:
+            raise ValueError("without slots the cache must hold at least one slot a sequence")
+    else:
+        _expect(slots, "slots", (n,), torch.int32)
+
+
+def delta_step(q, k, v, g, beta, states, slots=None, scale=None, out=None, prepare=False):
+    """out of the gated delta rule in its recurrent form, for decoding: the seqlen tokens (one,
+    or a few drafted ones) of each sequence, on states (nslots, nheads, headdim, dstate) float32,
+    which are updated in place.  slots (batch) int32: each sequence's slot (None: its index); a
+    slot outside the cache, or one that an earlier sequence names, marks padding, whose rows of
+    out stay as they were.  Other arguments as for delta_fwd."""
+    dims = _delta_check(q, k, v, g, beta, None, None)
+    batch, seqlen, H, P, G, N, _, io = dims
+    if not isinstance(states, torch.Tensor) or states.dim() != 4:
+        raise ValueError("states must be a 4-D tensor (nslots, nheads, headdim, dstate)")
+    nslots = states.shape[0]
+    _expect(states, "states", (nslots, H, P, N), torch.float32)
+    _check_slots(slots, batch, nslots)
+    _expect(out, "out", v.shape, io, required=False)
+    dev = _dev(q, k, v, g, beta, states, slots, out)
+    prob = _delta_problem(dims, False, scale)
+    if out is None:
+        out = torch.empty_like(v) if slots is None else torch.zeros_like(v)
+    args = (ctypes.byref(prob), _ptr(q), _ptr(k), _ptr(v), _ptr(g), _ptr(beta), _ptr(slots), nslots,
+            _ptr(states), _ptr(out), _stream(dev))
+    launch = _launcher(lib().ssd_delta_step, args, dev, prob)
+    if prepare:
+        return launch, out
+    launch()
+    return out
+
+
+# ------------------------------------------------------------ state cache ----
+CACHE_FORMATS = {torch.int8: 0, torch.float8_e4m3fn: 1}
+
+
+def _cache_problem(states_shape, codes, scales, slots):
+    """states_shape: (n, nheads, headdim, dstate)."""
+    if not isinstance(codes, torch.Tensor) or codes.dim() != 4:
+        raise ValueError("codes must be a 4-D tensor (nslots, nheads, headdim, dstate)")
+    if codes.dtype not in CACHE_FORMATS:
+        raise ValueError("codes must be int8 or float8_e4m3fn")
+    n, H, P, N = states_shape
+    nslots = codes.shape[0]
+    _expect(codes, "codes", (nslots, H, P, N), codes.dtype)
+    _expect(scales, "scales", (nslots, H, P), torch.float32)
+    _check_slots(slots, n, nslots)
+    return CacheProblem(n, nslots, H, P, N, CACHE_FORMATS[codes.dtype])
+
+
+def state_cache_write(states, codes, scales, slots=None, prepare=False):
+    """Park states (n, nheads, headdim, dstate) float32 in a cache's slots, 8 bits a value:
+    codes (nslots, nheads, headdim, dstate) int8 or float8_e4m3fn, scales (nslots, nheads,
+    headdim) float32 (include/ssd.h has the rounding).  slots (n) int32 (None: 0..n-1); a slot
+    outside the cache is not written, and of several sequences naming one slot the first is."""
+    if not isinstance(states, torch.Tensor) or states.dim() != 4:
+        raise ValueError("states must be a 4-D tensor (n, nheads, headdim, dstate)")
+    _expect(states, "states", states.shape, torch.float32)
+    prob = _cache_problem(tuple(states.shape), codes, scales, slots)
+    dev = _dev(states, codes, scales, slots)
+    args = (ctypes.byref(prob), _ptr(states), _ptr(slots), _ptr(codes), _ptr(scales), _stream(dev))
+    launch = _launcher(lib().ssd_state_cache_write, args, dev, prob)
+    if prepare:
+        return launch
+    launch()
+
+
+def state_cache_read(codes, scales, slots=None, out=None, prepare=False):
+    """The states parked in a cache's slots (every slot without `slots`): (n, nheads, headdim,
+    dstate) float32.  A slot outside the cache reads as a state of zeros."""
+    if not isinstance(codes, torch.Tensor) or codes.dim() != 4:
+        raise ValueError("codes must be a 4-D tensor (nslots, nheads, headdim, dstate)")
+    n = codes.shape[0] if slots is None else slots.numel()
+    shape = (n,) + tuple(codes.shape[1:])
+    prob = _cache_problem(shape, codes, scales, slots)
+    _expect(out, "out", shape, torch.float32, required=False)
+    dev = _dev(codes, scales, slots, out)
+    if out is None:
+        out = torch.empty(shape, dtype=torch.float32, device=dev)
+    args = (ctypes.byref(prob), _ptr(codes), _ptr(scales), _ptr(slots), _ptr(out), _stream(dev))
+    launch = _launcher(lib().ssd_state_cache_read, args, dev, prob)
+    if prepare:
+        return launch, out
+    launch()
+    return out

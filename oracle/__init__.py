@@ -26,6 +26,8 @@ Modules
 ``recurrence``  the literal token-by-token fp64 recurrence, forward and its
                 adjoint (backward) with segment checkpoints.  This is the
                 oracle the GPU path is checked against.
+``delta``       the gated delta rule token by token, its adjoint, and the state
+                cache's rounding.
 ``chunked``     the four-stage chunked form in fp64 (cumsum, chunk states,
                 state passing, chunk output) and its backward.  Used to pin
                 ``recurrence`` and to give per-stage intermediates.
