@@ -177,17 +177,26 @@ __device__ __forceinline__ Planes<IO::PI> raw_planes(const Raw8<IO>& x) {
   return f;
 }
 
-// 4 consecutive io elements <-> fp32
-__device__ __forceinline__ f32x4 load4(brsrc r, uint32_t off, IoBf16) {
-  typedef int i32x2 __attribute__((ext_vector_type(2)));
-  const i32x2 w = __builtin_bit_cast(i32x2, __builtin_amdgcn_raw_buffer_load_b64(r, off, 0, 0));
-  return f32x4{bf_lo(w[0]), bf_hi(w[0]), bf_lo(w[1]), bf_hi(w[1])};
-}
-__device__ __forceinline__ f32x4 load4(brsrc r, uint32_t off, IoF32) {
-  return __builtin_bit_cast(f32x4, buf_load16(r, off));
-}
+// 4 consecutive io elements: raw, as fp32, and stored.  (Raw where a load is used later:
+// widening a loaded value waits for it.)
+typedef uint32_t u32x2v __attribute__((ext_vector_type(2)));
+template <class IO>
+struct Raw4;
+template <>
+struct Raw4<IoBf16> {
+  u32x2v v;
+  __device__ __forceinline__ void load(brsrc r, uint32_t off) {
+    v = __builtin_bit_cast(u32x2v, __builtin_amdgcn_raw_buffer_load_b64(r, off, 0, 0));
+  }
+  __device__ __forceinline__ f32x4 get() const { return f32x4{bf_lo(v[0]), bf_hi(v[0]), bf_lo(v[1]), bf_hi(v[1])}; }
+};
+template <>
+struct Raw4<IoF32> {
+  u32x4 v;
+  __device__ __forceinline__ void load(brsrc r, uint32_t off) { v = buf_load16(r, off); }
+  __device__ __forceinline__ f32x4 get() const { return __builtin_bit_cast(f32x4, v); }
+};
 __device__ __forceinline__ void store4io(brsrc r, uint32_t off, f32x4 v, IoBf16) {
-  typedef uint32_t u32x2v __attribute__((ext_vector_type(2)));
   const u32x2v w = {pack_bf2(v[0], v[1]), pack_bf2(v[2], v[3])};
   __builtin_amdgcn_raw_buffer_store_b64(w, r, off, 0, 0);
 }
@@ -199,6 +208,35 @@ __device__ __forceinline__ void store4io(brsrc r, uint32_t off, f32x4 v, IoF32) 
 __device__ __forceinline__ float exp2_hl(float h, float l) {
   const float e = exp2_fast(h);
   return fmaf(e, l * 0.6931471805599453f, e);
+}
+
+// The chunk slots [c0, c1) and tokens [start, end) of sequence s, as scalars (uniform over
+// the workgroup: what is derived from them stays in scalar registers).
+struct SeqSpan {
+  int c0, c1, start, end;
+};
+__device__ __forceinline__ SeqSpan seq_span(const ChunkMap& m, int s) {
+  SeqSpan x;
+  if (!m.packed) {
+    x.c0 = s * m.ncs;
+    x.c1 = x.c0 + m.ncs;
+    x.start = s * m.seqlen;
+    x.end = x.start + m.seqlen;
+  } else {
+    x.c0 = min(m.seq_off[s], m.nck);
+    x.c1 = min(m.seq_off[s + 1], m.nck);
+    x.start = x.end = 0;
+    if (x.c1 > x.c0) {
+      const int4 a = m.tab[x.c0], b = m.tab[x.c1 - 1];
+      x.start = a.x;
+      x.end = b.x + b.y;
+    }
+  }
+  x.c0 = __builtin_amdgcn_readfirstlane(x.c0);
+  x.c1 = __builtin_amdgcn_readfirstlane(x.c1);
+  x.start = __builtin_amdgcn_readfirstlane(x.start);
+  x.end = __builtin_amdgcn_readfirstlane(x.end);
+  return x;
 }
 
 // A buffer offset that no resource covers (loads zero, stores nothing).

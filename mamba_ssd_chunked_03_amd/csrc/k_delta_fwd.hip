@@ -28,14 +28,13 @@ __global__ __launch_bounds__(256) void delta_fwd_kernel(DeltaArgs a) {
   __shared__ __align__(16) uint16_t Sl[PM * SPLANE];
   __shared__ __align__(16) uint16_t Xl[PM * XPLANE], Ul[PM * XPLANE], Wl[PM * XPLANE];
 
-  const int tid = threadIdx.x, w = tid >> 6, lane = tid & 63, q = lane >> 4, r = lane & 15;
+  const int tid = threadIdx.x, w = __builtin_amdgcn_readfirstlane(tid >> 6), lane = tid & 63, q = lane >> 4, r = lane & 15;
   const int np = a.P / PT;
   const int wg = xcd_order(blockIdx.x, gridDim.x);
   const int p0 = (wg % np) * PT, h = (wg / np) % a.H, s = wg / np / a.H;
   const int grp = h / (a.H / a.G);
-  int c0, c1;
-  seq_chunks(a.map, s, c0, c1);
-  c1 = min(c1, a.map.nck);
+  const SeqSpan sp = seq_span(a.map, s);
+  const int c0 = sp.c0, c1 = sp.c1;
 
   // the state: tile (i, t) of wave w holds columns 16 (w TW + i) + 4q + e, row p0 + 16t + r
   f32x4 S[TW][NT];
@@ -76,16 +75,13 @@ __global__ __launch_bounds__(256) void delta_fwd_kernel(DeltaArgs a) {
   struct Loads {
     Raw8<IO> k[KC], q[KS];
     u32x4 R[2][PM], P[2][PF];
-    f32x4 v[NT];
+    Raw4<IO> v[NT];
     float Gh, Gl, b, Ch, Cl;
-    int start, len;
   };
   auto load = [&](Loads& x, int c) {
-    const ChunkInfo ci = chunk_info(a.map, c);
-    x.start = ci.start;
-    x.len = ci.len;
-    const uint32_t row = (uint32_t)a.G * N * ES, span = (uint32_t)(ci.len - 1) * row + N * ES;
-    const int64_t base = ((int64_t)ci.start * a.G + grp) * N * ES;
+    const int start = sp.start + (c - c0) * C, len = min(C, sp.end - start);
+    const uint32_t row = (uint32_t)a.G * N * ES, span = (uint32_t)(len - 1) * row + N * ES;
+    const int64_t base = ((int64_t)start * a.G + grp) * N * ES;
     const brsrc rk = make_rsrc((const char*)a.k + base, span), rq = make_rsrc((const char*)a.q + base, span);
 #pragma unroll
     for (int i = 0; i < KC; ++i) {
@@ -107,10 +103,10 @@ __global__ __launch_bounds__(256) void delta_fwd_kernel(DeltaArgs a) {
       for (int e = 0; e < PF; ++e) x.P[S2][e] = *(const u32x4*)(P + e * kTriPlane + blk);
     }
     const uint32_t vrow = (uint32_t)a.H * a.P * ES;
-    const brsrc rv = make_rsrc((const char*)a.v + (((int64_t)ci.start * a.H + h) * a.P + p0) * ES,
-                               (uint32_t)(ci.len - 1) * vrow + PT * ES);
+    const brsrc rv = make_rsrc((const char*)a.v + (((int64_t)start * a.H + h) * a.P + p0) * ES,
+                               (uint32_t)(len - 1) * vrow + PT * ES);
 #pragma unroll
-    for (int t = 0; t < NT; ++t) x.v[t] = load4(rv, (16 * w + r) * vrow + (16 * t + 4 * q) * ES, IO{});
+    for (int t = 0; t < NT; ++t) x.v[t].load(rv, (16 * w + r) * vrow + (16 * t + 4 * q) * ES);
     const float* gt = a.gates + kh * (3 * C);
     x.Gh = gt[16 * w + r];
     x.Gl = gt[C + 16 * w + r];
@@ -159,7 +155,7 @@ __global__ __launch_bounds__(256) void delta_fwd_kernel(DeltaArgs a) {
     f32x4 X[NT];
 #pragma unroll
     for (int t = 0; t < NT; ++t) {
-      X[t] = x.v[t] - eG * ks_[t];
+      X[t] = x.v[t].get() - eG * ks_[t];
       uint2 o[PM];
       split4<PM>(b * X[t], o);
 #pragma unroll
@@ -175,7 +171,6 @@ __global__ __launch_bounds__(256) void delta_fwd_kernel(DeltaArgs a) {
 #pragma unroll
       for (int e = 0; e < PF; ++e) Pf[S2].p[e] = as_bf16x8(x.P[S2][e]);
     }
-    const int start = x.start, len = x.len;
     if (c + 1 < c1) load(x, c + 1);
     __syncthreads();
     // 2. Z = X - R (b X)
@@ -218,6 +213,7 @@ __global__ __launch_bounds__(256) void delta_fwd_kernel(DeltaArgs a) {
     put_state();
     // 4. the output (none where the backward recomputes what a forward keeps)
     if (a.out) {
+      const int start = sp.start + (c - c0) * C, len = min(C, sp.end - start);
       const uint32_t vrow = (uint32_t)a.H * a.P * ES;
       const brsrc ro = make_rsrc((char*)a.out + (((int64_t)start * a.H + h) * a.P + p0) * ES,
                                  (uint32_t)(len - 1) * vrow + PT * ES);

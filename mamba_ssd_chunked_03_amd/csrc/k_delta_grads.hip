@@ -1,0 +1,300 @@
+// Gated delta rule, gradients of q, k, g and beta, one workgroup per chunk and group of
+// heads, from what the chains kept: per head the state S entering the chunk, the adjoint
+// dS of the one leaving it, Z and F (U = b Z, dX = b F).  With
+//   dP = scale (dO U^T) . D (lower),  dM = -(dX U^T) . D (strictly lower):
+//   dq       = scale exp(G) dO S + dP K
+//   dk_read  = -exp(G) dX S + dM K            (k erasing)
+//   dk_write = exp(G_C - G) U dS + dP^T Q + dM^T K   (k written into the state)
+//   dbeta_i  = F_i . Z_i
+// The gates act through the running sum G only, and each row of Q, K enters with its
+// exp(+-G), so dL/dG_i = q_i . dq_i + k_i . dk_read_i - k_i . dk_write_i, plus
+// <S', dS> at the chunk's end for the whole decay (S' the state leaving it).  S' holds
+// the writes w_j = k_j . (exp(G_C - G) U dS)_j that dk_write takes out again: kept apart,
+// w_j enters dg_i as the sum over j < i and exp(G_C) <S, dS> alone is carried, instead of
+// two large sums that cancel.  dg is the suffix sum of dL/dG within the chunk.
+//
+// dq and dk are summed over the group's heads in registers, in order.  Eight waves: wave
+// w has tokens 16 (w % 4).. and one half of the N columns (w / 4); dP, dM are formed by
+// the two halves.
+#include "delta.hpp"
+
+namespace ssd {
+
+template <int N, int P, class IO>
+__global__ __launch_bounds__(512) void delta_grads_kernel(DeltaArgs a) {
+  using T = typename IO::T;
+  constexpr int PI = IO::PI, PM = IO::PM, ES = sizeof(T), C = kDeltaChunk, NTH = 512;
+  // columns of headdim staged at a time (the products' depth is 32; past P they are zero)
+  constexpr int PB = P < 32 ? 32 : (P > (PM == 2 ? 64 : 32) ? (PM == 2 ? 64 : 32) : P), NB = (P + PB - 1) / PB;
+  constexpr int LN = N + 8, LP = PB + 8, LC = C + 8;
+  constexpr int TN = N / 16, TH = (TN + 1) / 2;  // column tiles, of one half
+  constexpr int SPL = PB * LN, TPL = C * LP, KPL = C * LN, CPL = C * LC;
+  constexpr int PH1 = 2 * PM * SPL + (2 * PM + PI) * TPL, PH2 = 2 * PI * KPL + 2 * PM * CPL;
+  __shared__ __align__(16) uint16_t lds[PH1 > PH2 ? PH1 : PH2];
+  uint16_t *Sl = lds, *Dl = Sl + PM * SPL, *Ul = Dl + PM * SPL, *Xl = Ul + PM * TPL, *Ol = Xl + PM * TPL;
+  uint16_t *Kl = lds, *Ql = Kl + PI * KPL, *Pl = Ql + PI * KPL, *Ml = Pl + PM * CPL;
+  __shared__ float gl[3 * C], red[2][2][C], sd[NTH / 64], bsum[C];
+
+  const int tid = threadIdx.x, w = __builtin_amdgcn_readfirstlane(tid >> 6), lane = tid & 63, q = lane >> 4, r = lane & 15;
+  const int tb = w & 3, nh = w >> 2, tok = 16 * tb + r;
+  const int wg = xcd_order(blockIdx.x, gridDim.x);
+  const int ck = wg / a.G, grp = wg % a.G, per = a.H / a.G;
+  ChunkInfo ci = chunk_info(a.map, ck);
+  const int start = __builtin_amdgcn_readfirstlane(ci.start), len = __builtin_amdgcn_readfirstlane(ci.len);
+  if (len <= 0) return;
+  const uint32_t krow = (uint32_t)a.G * N * ES, kspan = (uint32_t)(len - 1) * krow + N * ES;
+  const int64_t kbase = ((int64_t)start * a.G + grp) * N * ES;
+  const brsrc rk = make_rsrc((const char*)a.k + kbase, kspan), rq = make_rsrc((const char*)a.q + kbase, kspan);
+  const uint32_t vrow = (uint32_t)a.H * P * ES;
+  const f32x4 zero = {0.f, 0.f, 0.f, 0.f};
+
+  f32x4 dqs[TH], dks[TH];
+#pragma unroll
+  for (int i = 0; i < TH; ++i) dqs[i] = dks[i] = zero;
+
+  for (int hh = 0; hh < per; ++hh) {
+    const int h = grp * per + hh;
+    const int64_t kh = (int64_t)ck * a.H + h;
+    const float* S = a.S + kh * P * N;
+    const float* dS = a.dS + kh * P * N;
+    const float* Z = a.Z + kh * C * P;
+    const float* F = a.F + kh * C * P;
+    const brsrc ro = make_rsrc((const char*)a.dout + ((int64_t)start * a.H + h) * P * ES,
+                               (uint32_t)(len - 1) * vrow + P * ES);
+    if (tid < 3 * C) gl[tid] = a.gates[kh * (3 * C) + tid];
+    f32x4 dq[TH], dr[TH], dw[TH], cc[4];
+#pragma unroll
+    for (int i = 0; i < TH; ++i) dq[i] = dr[i] = dw[i] = zero;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) cc[i] = zero;
+    float sdot = 0.f, bdot = 0.f;
+    __syncthreads();
+#pragma unroll 1
+    for (int pb = 0; pb < NB; ++pb) {
+      // stage the states (PB x N) and the token rows (64 x PB) as planes
+      constexpr int SE = PB * N / 4;
+#pragma unroll 4
+      for (int e = tid; e < SE; e += NTH) {
+        const int row = e / (N / 4), col = (e % (N / 4)) * 4, p = pb * PB + row;
+        f32x4 x = zero, y = zero;
+        if (p < P) {
+          x = *(const f32x4*)(S + (int64_t)p * N + col);
+          y = *(const f32x4*)(dS + (int64_t)p * N + col);
+        }
+        sdot += x[0] * y[0] + x[1] * y[1] + x[2] * y[2] + x[3] * y[3];
+        uint2 o[PM];
+        split4<PM>(x, o);
+#pragma unroll
+        for (int m = 0; m < PM; ++m) *(uint2*)(Sl + m * SPL + row * LN + col) = o[m];
+        split4<PM>(y, o);
+#pragma unroll
+        for (int m = 0; m < PM; ++m) *(uint2*)(Dl + m * SPL + row * LN + col) = o[m];
+      }
+      constexpr int PCS = PB / 8, TE = C * PCS;  // 8-element pieces; those of a token are adjacent lanes
+      if (tid < TE) {
+        const int t = tid / PCS, col = (tid % PCS) * 8, p = pb * PB + col;
+        f32x4 z0 = zero, z1 = zero, f0 = zero, f1 = zero;
+        if (p < P) {
+          z0 = *(const f32x4*)(Z + t * P + p);
+          z1 = *(const f32x4*)(Z + t * P + p + 4);
+          f0 = *(const f32x4*)(F + t * P + p);
+          f1 = *(const f32x4*)(F + t * P + p + 4);
+        }
+        Raw8<IO> o8;
+        o8.load(ro, p < P ? t * vrow + p * ES : kNoOffset);
+        const float b = gl[2 * C + t];
+        bdot += (z0[0] * f0[0] + z0[1] * f0[1] + z0[2] * f0[2] + z0[3] * f0[3]) +
+                (z1[0] * f1[0] + z1[1] * f1[1] + z1[2] * f1[2] + z1[3] * f1[3]);
+        u32x4 o[PM], oo[PI];
+        split8<PM>(b * z0, b * z1, o);
+#pragma unroll
+        for (int m = 0; m < PM; ++m) *(u32x4*)(Ul + m * TPL + t * LP + col) = o[m];
+        split8<PM>(b * f0, b * f1, o);
+#pragma unroll
+        for (int m = 0; m < PM; ++m) *(u32x4*)(Xl + m * TPL + t * LP + col) = o[m];
+        o8.planes(oo);
+#pragma unroll
+        for (int m = 0; m < PI; ++m) *(u32x4*)(Ol + m * TPL + t * LP + col) = oo[m];
+      }
+      __syncthreads();
+#pragma unroll 1
+      for (int ks = 0; ks < PB / 32; ++ks) {
+        const Planes<PI> of = lds_rows<PI>(Ol + 16 * tb * LP + 32 * ks, LP, TPL, lane);
+        const Planes<PM> xf = lds_rows<PM>(Xl + 16 * tb * LP + 32 * ks, LP, TPL, lane);
+        const Planes<PM> uf = lds_rows<PM>(Ul + 16 * tb * LP + 32 * ks, LP, TPL, lane);
+#pragma unroll
+        for (int i = 0; i < TH; ++i) {
+          const int nt = nh * TH + i;
+          if (nt < TN) {
+            const Planes<PM> sf = lds_cols<PM>(Sl + 32 * ks * LN + 16 * nt, LN, SPL, lane);
+            dq[i] = mma<PM>(sf, of, dq[i]);
+            dr[i] = mma<PM>(sf, xf, dr[i]);
+            dw[i] = mma<PM>(lds_cols<PM>(Dl + 32 * ks * LN + 16 * nt, LN, SPL, lane), uf, dw[i]);
+          }
+        }
+        // rows j (block J), columns i: the first half dO U^T, the second dX U^T
+#pragma unroll
+        for (int J = 0; J < 4; ++J)
+          if (J <= tb) {
+            const Planes<PM> jf = lds_rows<PM>(Ul + 16 * J * LP + 32 * ks, LP, TPL, lane);
+            cc[J] = nh == 0 ? mma<PM>(jf, of, cc[J]) : mma<PM>(jf, xf, cc[J]);
+          }
+      }
+      __syncthreads();
+    }
+    const float Gh = gl[tok], Gl = gl[C + tok];
+    const float eG = exp2_hl(Gh, Gl), eR = exp2_fast((gl[C - 1] - Gh) + (gl[2 * C - 1] - Gl));
+#pragma unroll
+    for (int i = 0; i < TH; ++i) {
+      dq[i] = (a.scale * eG) * dq[i];
+      dr[i] = -eG * dr[i];
+      dw[i] = eR * dw[i];
+    }
+    // dP (first half) or dM (second), [i][j]; the block right of an even diagonal one is read
+    // in the same step of 32 and written as zero
+    {
+      uint16_t* dst = nh == 0 ? Pl : Ml;
+      const float f = nh == 0 ? a.scale : -1.f;
+#pragma unroll
+      for (int J = 0; J < 4; ++J) {
+        if (J > tb && !(J == tb + 1 && (tb & 1) == 0)) continue;
+        f32x4 v = zero;
+        if (J <= tb) {
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const int j = 16 * J + 4 * q + e;
+            const float d = exp2_fast((Gh - gl[j]) + (Gl - gl[C + j]));
+            v[e] = (nh == 0 ? j <= tok : j < tok) ? f * (cc[J][e] * d) : 0.f;
+          }
+        }
+        uint2 o[PM];
+        split4<PM>(v, o);
+#pragma unroll
+        for (int m = 0; m < PM; ++m) *(uint2*)(dst + m * CPL + tok * LC + 16 * J + 4 * q) = o[m];
+      }
+    }
+    // K and Q
+    for (int e = tid; e < C * N / 8; e += NTH) {
+      const int t = e / (N / 8), col = (e % (N / 8)) * 8;
+      Raw8<IO> k8, q8;
+      k8.load(rk, t * krow + col * ES);
+      q8.load(rq, t * krow + col * ES);
+      u32x4 o[PI];
+      k8.planes(o);
+#pragma unroll
+      for (int m = 0; m < PI; ++m) *(u32x4*)(Kl + m * KPL + t * LN + col) = o[m];
+      q8.planes(o);
+#pragma unroll
+      for (int m = 0; m < PI; ++m) *(u32x4*)(Ql + m * KPL + t * LN + col) = o[m];
+    }
+    __syncthreads();
+    float da = 0.f, dwr = 0.f;  // this lane's part of dL/dG and of w
+#pragma unroll
+    for (int i = 0; i < TH; ++i) {
+      const int nt = nh * TH + i;
+      if (nt < TN) {
+        Raw4<IO> k4, q4;
+        k4.load(rk, tok * krow + (16 * nt + 4 * q) * ES);
+        q4.load(rq, tok * krow + (16 * nt + 4 * q) * ES);
+        const f32x4 w0 = dw[i];
+#pragma unroll
+        for (int ks = 0; ks < 2; ++ks) {
+          const Planes<PI> kf = lds_cols<PI>(Kl + 32 * ks * LN + 16 * nt, LN, KPL, lane);
+          if (ks == 0 || tb >= 2) {  // i in this block, j up to it
+            dq[i] = mma<PM>(kf, lds_rows<PM>(Pl + 16 * tb * LC + 32 * ks, LC, CPL, lane), dq[i]);
+            dr[i] = mma<PM>(kf, lds_rows<PM>(Ml + 16 * tb * LC + 32 * ks, LC, CPL, lane), dr[i]);
+          }
+          if (ks == 1 || tb < 2) {  // j in this block, i from it on
+            const Planes<PI> qf = lds_cols<PI>(Ql + 32 * ks * LN + 16 * nt, LN, KPL, lane);
+            dw[i] = mma<PM>(qf, lds_cols<PM>(Pl + 32 * ks * LC + 16 * tb, LC, CPL, lane), dw[i]);
+            dw[i] = mma<PM>(kf, lds_cols<PM>(Ml + 32 * ks * LC + 16 * tb, LC, CPL, lane), dw[i]);
+          }
+        }
+        const f32x4 kv = k4.get(), qv = q4.get();
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          da += qv[e] * dq[i][e] + kv[e] * (dr[i][e] - (dw[i][e] - w0[e]));
+          dwr += kv[e] * w0[e];
+        }
+        dqs[i] += dq[i];
+        dks[i] += dr[i] + dw[i];
+      }
+    }
+    da += __shfl_xor(da, 16);
+    da += __shfl_xor(da, 32);
+    dwr += __shfl_xor(dwr, 16);
+    dwr += __shfl_xor(dwr, 32);
+    if (q == 0) {
+      red[0][nh][tok] = da;
+      red[1][nh][tok] = dwr;
+    }
+    sdot = wave_sum(sdot);
+    if (lane == 0) sd[w] = sdot;
+    {
+      constexpr int PCS = PB / 8;
+#pragma unroll
+      for (int m = 1; m < PCS; m <<= 1) bdot += __shfl_xor(bdot, m);
+      if (tid < C * PCS && tid % PCS == 0) bsum[tid / PCS] = bdot;
+    }
+    __syncthreads();
+    if (w == 0) {
+      double x = (double)red[0][0][lane] + (double)red[0][1][lane];
+      double y = (double)red[1][0][lane] + (double)red[1][1][lane];
+      const double wj = y;
+      if (lane == C - 1) {
+        float t = 0.f;
+        for (int i = 0; i < NTH / 64; ++i) t += sd[i];
+        x += (double)(exp2_hl(gl[C - 1], gl[2 * C - 1]) * t);
+      }
+#pragma unroll
+      for (int d = 1; d < 64; d <<= 1) {
+        const double u = __shfl_down(x, d), v = __shfl_up(y, d);
+        if (lane + d < 64) x += u;
+        if (lane >= d) y += v;
+      }
+      if (lane < len) {
+        const int64_t at = ((int64_t)start + lane) * a.H + h;
+        a.dg[at] = (float)(x + (y - wj));
+        a.dbeta[at] = bsum[lane];
+      }
+    }
+    // (the next head's first barrier is behind these reads: gl is rewritten before it)
+    __syncthreads();
+  }
+  const brsrc wq = make_rsrc((char*)a.dq + kbase, kspan), wk = make_rsrc((char*)a.dk + kbase, kspan);
+#pragma unroll
+  for (int i = 0; i < TH; ++i) {
+    const int nt = nh * TH + i;
+    if (nt < TN) {
+      store4io(wq, tok * krow + (16 * nt + 4 * q) * ES, dqs[i], IO{});
+      store4io(wk, tok * krow + (16 * nt + 4 * q) * ES, dks[i], IO{});
+    }
+  }
+}
+
+hipError_t launch_delta_bwd_grads(const DeltaProb& p, const DeltaArgs& a, hipStream_t st) {
+  if (p.nck == 0) return hipSuccess;
+  const dim3 grid((unsigned)(p.nck * p.G)), block(512);
+  auto pick_p = [&](auto n, auto io) {
+    constexpr int N = decltype(n)::value;
+    using IO = decltype(io);
+    switch (p.P) {
+      case 16: hipLaunchKernelGGL((delta_grads_kernel<N, 16, IO>), grid, block, 0, st, a); break;
+      case 32: hipLaunchKernelGGL((delta_grads_kernel<N, 32, IO>), grid, block, 0, st, a); break;
+      case 64: hipLaunchKernelGGL((delta_grads_kernel<N, 64, IO>), grid, block, 0, st, a); break;
+      default: hipLaunchKernelGGL((delta_grads_kernel<N, 128, IO>), grid, block, 0, st, a); break;
+    }
+  };
+  auto pick = [&](auto io) {
+    switch (p.N) {
+      case 16: pick_p(std::integral_constant<int, 16>{}, io); break;
+      case 32: pick_p(std::integral_constant<int, 32>{}, io); break;
+      case 64: pick_p(std::integral_constant<int, 64>{}, io); break;
+      default: pick_p(std::integral_constant<int, 128>{}, io); break;
+    }
+  };
+  p.io ? pick(IoBf16{}) : pick(IoF32{});
+  return hipGetLastError();
+}
+
+}  // namespace ssd

@@ -44,10 +44,12 @@ __global__ __launch_bounds__(256) void delta_prep_kernel(DeltaArgs a, int hsplit
   __shared__ __align__(16) float mats[6][kDeltaChunk * kMatLd];
   float* KK = mats[4];
   float* QK = mats[5];
-  const int w = threadIdx.x >> 6, lane = threadIdx.x & 63, q = lane >> 4, r = lane & 15;
+  const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63, q = lane >> 4, r = lane & 15;
   const int wg = xcd_order(blockIdx.x, gridDim.x);
   const int hs = wg % hsplit, grp = (wg / hsplit) % a.G, ck = wg / hsplit / a.G;
-  const ChunkInfo ci = chunk_info(a.map, ck);
+  ChunkInfo ci = chunk_info(a.map, ck);
+  ci.start = __builtin_amdgcn_readfirstlane(ci.start);
+  ci.len = __builtin_amdgcn_readfirstlane(ci.len);
   if (ci.len <= 0) return;  // an unused slot
   const int per = a.H / a.G, h = grp * per + hs * 4 + w;
   const bool mine = hs * 4 + w < per;
