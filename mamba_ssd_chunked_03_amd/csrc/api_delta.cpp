@@ -81,7 +81,7 @@ DeltaLayout delta_layout(const DeltaProb& p) {
   };
   l.tab = take(p.packed ? (size_t)p.nck * 16 : 0);
   l.seq_off = take(p.packed ? ((size_t)p.nst + 1) * 4 : 0);
-  l.gates = take(ch * 3 * kDeltaChunk * 4);
+  l.gates = take(ch * kDeltaGates * 4);
   l.R = take(ch * PM * kTriPlane * 2);
   l.Pm = take(ch * PF * kTriPlane * 2);
   l.fwd_end = o;

@@ -57,7 +57,7 @@ struct DeltaArgs {
   const float *g, *beta, *init;
   void* out;
   float* final_states;
-  float* gates;                // (nck, H, 3, 64): running log2 decay (high, low part), beta
+  float* gates;                // (nck, H, kDeltaGates): see below
   uint16_t *R, *Pm, *Rt, *Pt;  // plane-split chunk matrices in fragment order (null: not kept)
   float *S, *Z;                // kept for the backward: states entering each chunk, Z
   // backward
@@ -68,6 +68,13 @@ struct DeltaArgs {
   float *dg, *dbeta;
 };
 
+// Per (chunk, head), 64 tokens each: running log2 decay G (high part, low part), beta; and
+// where io is bf16 exp(G), exp(G_C - G).  Past the chunk's end G stays and beta is zero.
+constexpr int kDeltaGates = 5 * kDeltaChunk;
+
+hipError_t launch_delta_f32_prep(const DeltaProb& p, const DeltaArgs& a, hipStream_t st);
+hipError_t launch_delta_f32_fwd(const DeltaProb& p, const DeltaArgs& a, hipStream_t st);
+hipError_t launch_delta_f32_bwd(const DeltaProb& p, const DeltaArgs& a, hipStream_t st);
 hipError_t launch_delta_prep(const DeltaProb& p, const DeltaArgs& a, hipStream_t st);
 hipError_t launch_delta_fwd(const DeltaProb& p, const DeltaArgs& a, hipStream_t st);
 hipError_t launch_delta_bwd_chain(const DeltaProb& p, const DeltaArgs& a, hipStream_t st);

@@ -1,0 +1,62 @@
+// Tiles of the bf16 kernels of the gated delta rule that stay in registers.
+//
+// A product's accumulator tile D (16 x 16) leaves lane (q, r) with rows 4q..4q+3 of
+// column r, and an MFMA operand of depth 32 wants 8 consecutive depths 8q..8q+7 in lane
+// group q.  Rows of a 32-row block are therefore dealt to its two tiles (t = 0, 1) so
+// that row 4q + e of tile t is row 8q + 4t + e of the block: the two tiles' registers,
+// side by side, are then an operand of the next product (the contraction running over
+// those rows) with nothing moved between lanes.  Operand rows are read in the same
+// order (row32 below); a transposing LDS read takes its four groups of four columns
+// eight apart (cols32).
+#pragma once
+
+#include "delta.hpp"
+
+namespace ssd {
+
+// row of a 32-row block that operand row r (0..15) of tile t stands for
+__device__ __forceinline__ int row32(int r, int t) { return 8 * (r >> 2) + 4 * t + (r & 3); }
+
+// Lower triangular 64 x 64 matrices (R, P) in operand order: row tile (B, t), column
+// block S <= B; transposed ones: row tile (S, t), column block B >= S.
+__host__ __device__ __forceinline__ int low_block(int B, int t, int S) { return B == 0 ? t : 2 + 2 * t + S; }
+__host__ __device__ __forceinline__ int up_block(int S, int t, int B) { return S == 1 ? 4 + t : 2 * t + B; }
+
+// Operand from an LDS tile stored [k][col] (row stride ld): depths k = 8q..8q+7, operand
+// row 4g + e <-> column 8g + 4t + e (t the tile of a 32-column block).  `p` points at
+// [k0][col0].
+__device__ __forceinline__ bf16x8 cols32(const uint16_t* tile, int ld, int t, int lane) {
+  const int j = lane & 15;
+  const uint16_t* p = tile + (8 * (lane >> 4) + (j >> 2)) * ld + 8 * (j & 3) + 4 * t;
+  v4i16 a = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4i16*)p);
+  v4i16 b = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4i16*)(p + 4 * ld));
+  v8i16 c = __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7);
+  return __builtin_bit_cast(bf16x8, c);
+}
+
+// two tiles (rows 8q + 0..3, 8q + 4..7 of a 32-row block) -> operand planes
+template <int NP>
+__device__ __forceinline__ Planes<NP> tile_planes(f32x4 a, f32x4 b) {
+  u32x4 o[NP];
+  split8<NP>(a, b, o);
+  Planes<NP> f;
+#pragma unroll
+  for (int i = 0; i < NP; ++i) f.p[i] = as_bf16x8(o[i]);
+  return f;
+}
+
+// acc += a (one plane) times every plane of b, and the other way round (transposed tile)
+template <int NP>
+__device__ __forceinline__ f32x4 mma1(bf16x8 a, const Planes<NP>& b, f32x4 c) {
+#pragma unroll
+  for (int i = NP - 1; i >= 0; --i) c = mfma_bf16(a, b.p[i], c);
+  return c;
+}
+template <int NP>
+__device__ __forceinline__ f32x4 mma1t(const Planes<NP>& a, bf16x8 b, f32x4 c) {
+#pragma unroll
+  for (int i = NP - 1; i >= 0; --i) c = mfma_bf16(a.p[i], b, c);
+  return c;
+}
+
+}  // namespace ssd

@@ -1,266 +1,274 @@
-// Gated delta rule, backward chain: the reverse walk over one sequence's chunks for PT
-// columns of headdim of one head, with the adjoint dS of the state leaving the chunk in
-// registers (fp32), from what the forward kept (R and P transposed, the gates).  With
-// U = b Z and O = scale exp(G) Q S^T + P U, per chunk:
-//   1. E = P^T dO + exp(G_C - G) K dS^T            (adjoint of U)
-//   2. F = E - R^T (b E), dX = b F = dV             (adjoints of U in full, and of X)
-//   3. dS <- exp(G_C) dS + (scale exp(G) dO)^T Q - (exp(G) dX)^T K
+// Gated delta rule, bf16 io, backward chain: the reverse walk over one sequence's chunks
+// for 16 columns of headdim of one head a wave, with the adjoint dS of the state leaving
+// the chunk in registers, from what the forward kept (R and P transposed, the gates).
+// With U = b Z and O = scale exp(G) Q S^T + P U, per chunk:
+//   E = P^T dO + exp(G_C - G) K dS^T          (adjoint of U)
+//   F = E - R^T (b E),   dX = b F = dV         (adjoints of U in full, and of X)
+//   dS <- exp(G_C) dS + (scale exp(G) dO)^T Q - (exp(G) dX)^T K
 // F and the dS of every chunk are stored for k_delta_grads.hip, which forms the other
-// gradients chunk by chunk.  Layout, planes and barriers as in k_delta_fwd.hip.
-#include "delta.hpp"
+// gradients chunk by chunk.  Registers, staging and the split over waves are those of
+// k_delta_fwd.hip; two planes throughout.
+#include "delta_reg.hpp"
 
 namespace ssd {
 
-template <int N, int PT, class IO>
-__global__ __launch_bounds__(256) void delta_bwd_chain_kernel(DeltaArgs a) {
-  using T = typename IO::T;
-  constexpr int PI = IO::PI, PM = IO::PM, ES = sizeof(T);
-  constexpr int NP = N < 32 ? 32 : N, KS = NP / 32, NT = PT / 16;
-  constexpr int TN = N / 16, TW = (TN + 3) / 4;
-  constexpr int LK = NP + 8, LX = PT;
-  constexpr int C = kDeltaChunk, KPLANE = C * LK, SPLANE = PT * LK, XPLANE = C * LX;
-  __shared__ __align__(16) uint16_t Kl[PI * KPLANE], Ql[PI * KPLANE];
-  __shared__ __align__(16) uint16_t Sl[PM * SPLANE];
-  __shared__ __align__(16) uint16_t Ol[PI * XPLANE], Dl[PM * XPLANE];  // dO, scale exp(G) dO
-  __shared__ __align__(16) uint16_t Xl[PM * XPLANE], Wl[PM * XPLANE];  // b E, -exp(G) dX
+template <int N, int NS>
+__global__ __launch_bounds__(256, 1) void delta_bwd_kernel(DeltaArgs a, int ptiles) {
+  constexpr int C = kDeltaChunk, NP = N < 32 ? 32 : N, KS = NP / 32, KW = (KS + NS - 1) / NS, NPT = 4 / NS;
+  constexpr int LK = NP + 8, LV = 16 * NPT + 8;
+  constexpr int EK = C * LK, ER = 2 * kTriPlane, EV = C * LV;
+  struct Buf {
+    uint16_t K[EK], Q[EK], R[ER], P[ER], O[EV];
+    float g[3 * C];  // beta, exp(G), exp(G_C - G)
+  };
+  __shared__ __align__(16) Buf buf[2];
+  constexpr int XCH = NS > 1 ? NPT * NS * 4 * 64 : 1;
+  __shared__ __align__(16) f32x4 xk[XCH];
 
   const int tid = threadIdx.x, w = __builtin_amdgcn_readfirstlane(tid >> 6), lane = tid & 63, q = lane >> 4, r = lane & 15;
-  const int np = a.P / PT;
+  const int pt = w / NS, ns = w % NS;
+  const int np = (ptiles + NPT - 1) / NPT;
   const int wg = xcd_order(blockIdx.x, gridDim.x);
-  const int p0 = (wg % np) * PT, h = (wg / np) % a.H, s = wg / np / a.H;
+  const int pg = wg % np, h = (wg / np) % a.H, s = wg / np / a.H;
+  const int p0 = pg * 16 * NPT;
+  const int pw = 16 * min(NPT, ptiles - pg * NPT);
+  const bool live = 16 * pt < pw;
+  const int pc = p0 + 16 * pt + r;
   const int grp = h / (a.H / a.G);
   const SeqSpan sp = seq_span(a.map, s);
   const int c0 = sp.c0, c1 = sp.c1;
+  const f32x4 zero = {0.f, 0.f, 0.f, 0.f};
 
-  f32x4 S[TW][NT];
-  const int64_t sbase = ((int64_t)s * a.H + h) * a.P * N;
+  f32x4 S[KW][2];
+  const int64_t srow = (((int64_t)s * a.H + h) * a.P + pc) * N;
+  auto scol = [&](int k, int t) { return 32 * (ns * KW + k) + 8 * q + 4 * t; };
 #pragma unroll
-  for (int i = 0; i < TW; ++i)
+  for (int k = 0; k < KW; ++k)
 #pragma unroll
-    for (int t = 0; t < NT; ++t) {
-      const int nt = w * TW + i;
-      S[i][t] = a.d_final && nt < TN
-                    ? *(const f32x4*)(a.d_final + sbase + (int64_t)(p0 + 16 * t + r) * N + 16 * nt + 4 * q)
-                    : f32x4{0.f, 0.f, 0.f, 0.f};
-    }
-  auto put_state = [&]() {
-#pragma unroll
-    for (int i = 0; i < TW; ++i)
-#pragma unroll
-      for (int t = 0; t < NT; ++t) {
-        const int nt = w * TW + i;
-        if (nt < TN) {
-          uint2 o[PM];
-          split4<PM>(S[i][t], o);
-#pragma unroll
-          for (int e = 0; e < PM; ++e)
-            *(uint2*)(Sl + e * SPLANE + (16 * t + r) * LK + 16 * nt + 4 * q) = o[e];
-        }
-      }
-  };
+    for (int t = 0; t < 2; ++t)
+      S[k][t] = a.d_final && live && scol(k, t) < N ? *(const f32x4*)(a.d_final + srow + scol(k, t)) : zero;
+
   if constexpr (N < 32) {
-    for (int e = tid; e < PI * C; e += 256)
-      for (int c = N; c < 32; c += 4) *(uint2*)(Kl + e * LK + c) = make_uint2(0u, 0u);
-    for (int e = tid; e < PM * PT; e += 256)
-      for (int c = N; c < 32; c += 4) *(uint2*)(Sl + e * LK + c) = make_uint2(0u, 0u);
+    for (int e = tid; e < 2 * C; e += 256)
+      for (int c = N; c < 32; c += 4) {
+        *(uint2*)(buf[e / C].K + (e % C) * LK + c) = make_uint2(0u, 0u);
+        *(uint2*)(buf[e / C].Q + (e % C) * LK + c) = make_uint2(0u, 0u);
+      }
   }
-  put_state();
 
-  constexpr int PC = N / 8, KC = (C * PC + 255) / 256;
+  constexpr int KC = (C * N / 8 + 255) / 256, RC = ER / 8 / 256, VP = 2 * NPT, VC = (C * VP + 255) / 256;
   struct Loads {
-    Raw8<IO> k[KC], q[KC];
-    u32x4 R[2][PM], P[2][PM];
-    Raw4<IO> o[NT];
-    float Gh, Gl, b, Ch, Cl;
+    u32x4 k[KC], q[KC], R[RC], P[RC], o[VC];
+    float g;
   };
   auto load = [&](Loads& x, int c) {
     const int start = sp.start + (c - c0) * C, len = min(C, sp.end - start);
-    const uint32_t row = (uint32_t)a.G * N * ES, span = (uint32_t)(len - 1) * row + N * ES;
-    const int64_t base = ((int64_t)start * a.G + grp) * N * ES;
+    const uint32_t row = (uint32_t)a.G * N * 2, span = (uint32_t)(len - 1) * row + N * 2;
+    const int64_t base = ((int64_t)start * a.G + grp) * N * 2;
     const brsrc rk = make_rsrc((const char*)a.k + base, span), rq = make_rsrc((const char*)a.q + base, span);
 #pragma unroll
     for (int i = 0; i < KC; ++i) {
       const int e = tid + i * 256;
-      const uint32_t off = e < C * PC ? (e / PC) * row + (e % PC) * 8 * ES : kNoOffset;
-      x.k[i].load(rk, off);
-      x.q[i].load(rq, off);
+      const uint32_t off = e < C * N / 8 ? (e / (N / 8)) * row + (e % (N / 8)) * 16 : kNoOffset;
+      x.k[i] = buf_load16(rk, off);
+      x.q[i] = buf_load16(rq, off);
     }
     const int64_t kh = (int64_t)c * a.H + h;
-    const uint16_t* R = a.Rt + kh * (PM * kTriPlane) + lane * 8;
-    const uint16_t* P = a.Pt + kh * (PM * kTriPlane) + lane * 8;
+    const brsrc rr = make_rsrc(a.Rt + kh * ER, ER * 2), rp = make_rsrc(a.Pt + kh * ER, ER * 2);
 #pragma unroll
-    for (int S2 = 0; S2 < 2; ++S2) {
-      const int blk = trit_block(w, w < 2 ? S2 : 1) * 512;  // (waves 2, 3: block 0 is not used)
-#pragma unroll
-      for (int e = 0; e < PM; ++e) {
-        x.R[S2][e] = *(const u32x4*)(R + e * kTriPlane + blk);
-        x.P[S2][e] = *(const u32x4*)(P + e * kTriPlane + blk);
-      }
+    for (int i = 0; i < RC; ++i) {
+      x.R[i] = buf_load16(rr, (tid + i * 256) * 16);
+      x.P[i] = buf_load16(rp, (tid + i * 256) * 16);
     }
-    const uint32_t vrow = (uint32_t)a.H * a.P * ES;
-    const brsrc ro = make_rsrc((const char*)a.dout + (((int64_t)start * a.H + h) * a.P + p0) * ES,
-                               (uint32_t)(len - 1) * vrow + PT * ES);
+    const uint32_t vrow = (uint32_t)a.H * a.P * 2;
+    const brsrc ro = make_rsrc((const char*)a.dout + (((int64_t)start * a.H + h) * a.P + p0) * 2,
+                               (uint32_t)(len - 1) * vrow + pw * 2);
 #pragma unroll
-    for (int t = 0; t < NT; ++t) x.o[t].load(ro, (16 * w + r) * vrow + (16 * t + 4 * q) * ES);
-    const float* gt = a.gates + kh * (3 * C);
-    x.Gh = gt[16 * w + r];
-    x.Gl = gt[C + 16 * w + r];
-    x.b = gt[2 * C + 16 * w + r];
-    x.Ch = gt[C - 1];
-    x.Cl = gt[2 * C - 1];
+    for (int i = 0; i < VC; ++i) {
+      const int e = tid + i * 256;
+      x.o[i] = buf_load16(ro, e < C * VP && 8 * (e % VP) < pw ? (e / VP) * vrow + (e % VP) * 16 : kNoOffset);
+    }
+    x.g = tid < 3 * C ? a.gates[kh * kDeltaGates + 2 * C + tid] : 0.f;
   };
-  const int xo = (16 * w + r) * LX + 4 * q;
-  auto put_chunk = [&](const Loads& x) {
+  auto put = [&](const Loads& x, Buf& b) {
 #pragma unroll
     for (int i = 0; i < KC; ++i) {
       const int e = tid + i * 256;
-      u32x4 k[PI], qq[PI];
-      x.k[i].planes(k);
-      x.q[i].planes(qq);
-      if (e < C * PC)
-#pragma unroll
-        for (int m = 0; m < PI; ++m) {
-          *(u32x4*)(Kl + m * KPLANE + (e / PC) * LK + (e % PC) * 8) = k[m];
-          *(u32x4*)(Ql + m * KPLANE + (e / PC) * LK + (e % PC) * 8) = qq[m];
-        }
+      if (e < C * N / 8) {
+        *(u32x4*)(b.K + (e / (N / 8)) * LK + (e % (N / 8)) * 8) = x.k[i];
+        *(u32x4*)(b.Q + (e / (N / 8)) * LK + (e % (N / 8)) * 8) = x.q[i];
+      }
     }
-    const float se = a.scale * exp2_hl(x.Gh, x.Gl);
 #pragma unroll
-    for (int t = 0; t < NT; ++t) {
-      const f32x4 o = x.o[t].get();
-      uint2 p[PI], d[PM];
-      split4<PI>(o, p);
-      split4<PM>(se * o, d);
-#pragma unroll
-      for (int e = 0; e < PI; ++e) *(uint2*)(Ol + e * XPLANE + xo + 16 * t) = p[e];
-#pragma unroll
-      for (int e = 0; e < PM; ++e) *(uint2*)(Dl + e * XPLANE + xo + 16 * t) = d[e];
+    for (int i = 0; i < RC; ++i) {
+      *(u32x4*)(b.R + (tid + i * 256) * 8) = x.R[i];
+      *(u32x4*)(b.P + (tid + i * 256) * 8) = x.P[i];
     }
+#pragma unroll
+    for (int i = 0; i < VC; ++i) {
+      const int e = tid + i * 256;
+      if (e < C * VP) *(u32x4*)(b.O + (e / VP) * LV + (e % VP) * 8) = x.o[i];
+    }
+    if (tid < 3 * C) b.g[tid] = x.g;
   };
 
   Loads x;
   if (c0 < c1) {
     load(x, c1 - 1);
-    put_chunk(x);
+    put(x, buf[0]);
+    if (c1 - 2 >= c0) load(x, c1 - 2);
   }
   __syncthreads();
-  const f32x4 zero = {0.f, 0.f, 0.f, 0.f};
   for (int c = c1 - 1; c >= c0; --c) {
+    const Buf& b = buf[(c1 - 1 - c) & 1];
     const int64_t kh = (int64_t)c * a.H + h;
-    const float eG = exp2_hl(x.Gh, x.Gl), eC = exp2_hl(x.Ch, x.Cl);
-    const float eR = exp2_fast((x.Ch - x.Gh) + (x.Cl - x.Gl)), b = x.b;
-    // 1. E
-    Planes<PM> Rf[2], Pf[2];
+    f32x4 ks[2][2];
 #pragma unroll
-    for (int S2 = 0; S2 < 2; ++S2)
+    for (int i = 0; i < 4; ++i) ks[i >> 1][i & 1] = zero;
 #pragma unroll
-      for (int e = 0; e < PM; ++e) {
-        Rf[S2].p[e] = as_bf16x8(x.R[S2][e]);
-        Pf[S2].p[e] = as_bf16x8(x.P[S2][e]);
-      }
-    f32x4 E[NT];
+    for (int k = 0; k < KW; ++k) {
+      const int kk = ns * KW + k;
+      if (KS % NS == 0 || kk < KS) {
+        const Planes<2> sf = tile_planes<2>(S[k][0], S[k][1]);
+        if (live)
 #pragma unroll
-    for (int t = 0; t < NT; ++t) E[t] = zero;
+          for (int t = 0; t < 2; ++t)
+            if (scol(k, t) < N) *(f32x4*)(a.dS + (kh * a.P + pc) * N + scol(k, t)) = S[k][t];
 #pragma unroll
-    for (int ks = 0; ks < KS; ++ks) {
-      const Planes<PI> kf = lds_rows<PI>(Kl + 16 * w * LK + 32 * ks, LK, KPLANE, lane);
+        for (int B = 0; B < 2; ++B)
 #pragma unroll
-      for (int t = 0; t < NT; ++t)
-        E[t] = mma<PM>(lds_rows<PM>(Sl + 16 * t * LK + 32 * ks, LK, SPLANE, lane), kf, E[t]);
-    }
-#pragma unroll
-    for (int t = 0; t < NT; ++t) {
-      f32x4 e = eR * E[t];
-      e = mma<PM>(lds_cols<PI>(Ol + 32 * LX + 16 * t, LX, XPLANE, lane), Pf[1], e);
-      if (w < 2) e = mma<PM>(lds_cols<PI>(Ol + 16 * t, LX, XPLANE, lane), Pf[0], e);
-      E[t] = e;
-      uint2 o[PM];
-      split4<PM>(b * e, o);
-#pragma unroll
-      for (int m = 0; m < PM; ++m) *(uint2*)(Xl + m * XPLANE + xo + 16 * t) = o[m];
-    }
-    if (c > c0) load(x, c - 1);
-    __syncthreads();
-    // 2. F, dX
-    {
-      const int start = sp.start + (c - c0) * C, len = min(C, sp.end - start);
-      const uint32_t vrow = (uint32_t)a.H * a.P * ES;
-      const brsrc rv = make_rsrc((char*)a.dv + (((int64_t)start * a.H + h) * a.P + p0) * ES,
-                                 (uint32_t)(len - 1) * vrow + PT * ES);
-#pragma unroll
-      for (int t = 0; t < NT; ++t) {
-        f32x4 f = zero;
-        f = mma<PM>(lds_cols<PM>(Xl + 32 * LX + 16 * t, LX, XPLANE, lane), Rf[1], f);
-        if (w < 2) f = mma<PM>(lds_cols<PM>(Xl + 16 * t, LX, XPLANE, lane), Rf[0], f);
-        f = E[t] - f;
-        *(f32x4*)(a.F + (kh * C + 16 * w + r) * a.P + p0 + 16 * t + 4 * q) = f;
-        const f32x4 dx = b * f;
-        store4io(rv, (16 * w + r) * vrow + (16 * t + 4 * q) * ES, dx, IO{});
-        uint2 o[PM];
-        split4<PM>(-eG * dx, o);
-#pragma unroll
-        for (int m = 0; m < PM; ++m) *(uint2*)(Wl + m * XPLANE + xo + 16 * t) = o[m];
+          for (int t = 0; t < 2; ++t)
+            ks[B][t] = mma1<2>(as_bf16x8(*(const u32x4*)(b.K + (32 * B + row32(r, t)) * LK + 32 * kk + 8 * q)), sf, ks[B][t]);
       }
     }
-    __syncthreads();
-    // 3. dS
+    if constexpr (NS > 1) {
 #pragma unroll
-    for (int i = 0; i < TW; ++i) {
-      const int nt = w * TW + i;
-      if (nt < TN) {
-        Planes<PI> kf[2], qf[2];
-#pragma unroll
-        for (int S2 = 0; S2 < 2; ++S2) {
-          kf[S2] = lds_cols<PI>(Kl + 32 * S2 * LK + 16 * nt, LK, KPLANE, lane);
-          qf[S2] = lds_cols<PI>(Ql + 32 * S2 * LK + 16 * nt, LK, KPLANE, lane);
-        }
-#pragma unroll
-        for (int t = 0; t < NT; ++t) {
-          *(f32x4*)(a.dS + (kh * a.P + p0 + 16 * t + r) * N + 16 * nt + 4 * q) = S[i][t];
-          f32x4 acc = eC * S[i][t];
-#pragma unroll
-          for (int S2 = 0; S2 < 2; ++S2) {
-            acc = mma<PM>(qf[S2], lds_cols<PM>(Dl + 32 * S2 * LX + 16 * t, LX, XPLANE, lane), acc);
-            acc = mma<PM>(kf[S2], lds_cols<PM>(Wl + 32 * S2 * LX + 16 * t, LX, XPLANE, lane), acc);
-          }
-          S[i][t] = acc;
-        }
-      }
-    }
-    put_state();
-    __syncthreads();
-    if (c > c0) {
-      put_chunk(x);
+      for (int i = 0; i < 4; ++i) xk[((pt * NS + ns) * 4 + i) * 64 + lane] = ks[i >> 1][i & 1];
       __syncthreads();
-    }
-  }
-  if (a.d_init) {
 #pragma unroll
-    for (int i = 0; i < TW; ++i)
+      for (int i = 0; i < 4; ++i) {
+        f32x4 y = xk[(pt * NS * 4 + i) * 64 + lane];
 #pragma unroll
-      for (int t = 0; t < NT; ++t) {
-        const int nt = w * TW + i;
-        if (nt < TN) *(f32x4*)(a.d_init + sbase + (int64_t)(p0 + 16 * t + r) * N + 16 * nt + 4 * q) = S[i][t];
+        for (int j = 1; j < NS; ++j) y += xk[((pt * NS + j) * 4 + i) * 64 + lane];
+        ks[i >> 1][i & 1] = y;
       }
+    }
+    auto tri = [&](const uint16_t* m, int S2, int t, int B) {
+      Planes<2> f;
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+        f.p[i] = as_bf16x8(*(const u32x4*)(m + i * kTriPlane + up_block(S2, t, B) * 512 + lane * 8));
+      return f;
+    };
+    // E: tile (B, t) has tokens 32B + 8q + 4t + e
+    f32x4 E[2][2], bt[2][2], eg[2][2];
+    Planes<2> ef[2], of2[2];
+    bf16x8 of[2];
+#pragma unroll
+    for (int B = 0; B < 2; ++B) of[B] = frag_kmajor(b.O + 32 * B * LV + 16 * pt, LV, lane);
+#pragma unroll
+    for (int B = 0; B < 2; ++B) {
+#pragma unroll
+      for (int t = 0; t < 2; ++t) {
+        const int tk = 32 * B + 8 * q + 4 * t;
+        bt[B][t] = *(const f32x4*)(b.g + tk);
+        eg[B][t] = *(const f32x4*)(b.g + C + tk);
+        f32x4 e = *(const f32x4*)(b.g + 2 * C + tk) * ks[B][t];
+#pragma unroll
+        for (int B2 = 1; B2 >= B; --B2) e = mma1t<2>(tri(b.P, B, t, B2), of[B2], e);
+        E[B][t] = e;
+      }
+      ef[B] = tile_planes<2>(bt[B][0] * E[B][0], bt[B][1] * E[B][1]);
+      const u32x4 ow = __builtin_bit_cast(u32x4, of[B]);
+      f32x4 o[2];
+#pragma unroll
+      for (int t = 0; t < 2; ++t)
+        o[t] = (a.scale * eg[B][t]) *
+               f32x4{bf_lo(ow[2 * t]), bf_hi(ow[2 * t]), bf_lo(ow[2 * t + 1]), bf_hi(ow[2 * t + 1])};
+      of2[B] = tile_planes<2>(o[0], o[1]);
+    }
+    const int start = sp.start + (c - c0) * C, len = min(C, sp.end - start);
+    uint16_t* dv = (uint16_t*)a.dv + ((int64_t)start * a.H + h) * a.P + pc;
+    Planes<2> wf[2];
+#pragma unroll
+    for (int B = 0; B < 2; ++B) {
+      f32x4 wv[2];
+#pragma unroll
+      for (int t = 0; t < 2; ++t) {
+        f32x4 f = zero;
+#pragma unroll
+        for (int B2 = 1; B2 >= B; --B2) f = mma<2>(tri(b.R, B, t, B2), ef[B2], f);
+        f = E[B][t] - f;
+        const f32x4 dx = bt[B][t] * f;
+        wv[t] = -eg[B][t] * dx;
+        if (live && (NS == 1 || (2 * B + t) % NS == ns)) {
+          const int tk = 32 * B + 8 * q + 4 * t;
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            a.F[(kh * C + tk + e) * a.P + pc] = f[e];
+            if (tk + e < len) dv[(int64_t)(tk + e) * a.H * a.P] = f2bf(dx[e]);
+          }
+        }
+      }
+      wf[B] = tile_planes<2>(wv[0], wv[1]);
+    }
+    const float eC = b.g[C + C - 1];
+#pragma unroll
+    for (int k = 0; k < KW; ++k) {
+      const int kk = ns * KW + k;
+      if (KS % NS == 0 || kk < KS) {
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+          f32x4 y = eC * S[k][t];
+#pragma unroll
+          for (int B = 0; B < 2; ++B) {
+            y = mma1<2>(cols32(b.Q + 32 * B * LK + 32 * kk, LK, t, lane), of2[B], y);
+            y = mma1<2>(cols32(b.K + 32 * B * LK + 32 * kk, LK, t, lane), wf[B], y);
+          }
+          S[k][t] = y;
+        }
+      }
+    }
+    if (c > c0) {
+      put(x, buf[(c1 - c) & 1]);
+      if (c - 2 >= c0) load(x, c - 2);
+    }
+    __syncthreads();
+  }
+  if (a.d_init && live) {
+#pragma unroll
+    for (int k = 0; k < KW; ++k)
+#pragma unroll
+      for (int t = 0; t < 2; ++t)
+        if (scol(k, t) < N) *(f32x4*)(a.d_init + srow + scol(k, t)) = S[k][t];
   }
 }
 
 hipError_t launch_delta_bwd_chain(const DeltaProb& p, const DeltaArgs& a, hipStream_t st) {
+  if (!p.io) return launch_delta_f32_bwd(p, a, st);
   if (p.nst == 0) return hipSuccess;
-  auto go = [&](auto n, auto io) {
-    constexpr int PT = 16;
-    hipLaunchKernelGGL((delta_bwd_chain_kernel<decltype(n)::value, PT, decltype(io)>),
-                       dim3((unsigned)((int64_t)p.nst * p.H * (p.P / PT))), dim3(256), 0, st, a);
+  const int ptiles = p.P / 16;
+  const int64_t heads = (int64_t)p.nst * p.H;
+  auto go = [&](auto n, auto ns) {
+    constexpr int NS = decltype(ns)::value, NPT = 4 / NS;
+    hipLaunchKernelGGL((delta_bwd_kernel<decltype(n)::value, NS>),
+                       dim3((unsigned)(heads * ((ptiles + NPT - 1) / NPT))), dim3(256), 0, st, a, ptiles);
   };
-  auto pick = [&](auto io) {
-    switch (p.N) {
-      case 16: go(std::integral_constant<int, 16>{}, io); break;
-      case 32: go(std::integral_constant<int, 32>{}, io); break;
-      case 64: go(std::integral_constant<int, 64>{}, io); break;
-      default: go(std::integral_constant<int, 128>{}, io); break;
-    }
+  auto pick = [&](auto n) {
+    const int64_t tiles = heads * ptiles;
+    if (tiles >= 512 && ptiles >= 4)
+      go(n, std::integral_constant<int, 1>{});
+    else if (tiles >= 256 && ptiles >= 2)
+      go(n, std::integral_constant<int, 2>{});
+    else
+      go(n, std::integral_constant<int, 4>{});
   };
-  p.io ? pick(IoBf16{}) : pick(IoF32{});
+  switch (p.N) {
+    case 16: pick(std::integral_constant<int, 16>{}); break;
+    case 32: pick(std::integral_constant<int, 32>{}); break;
+    case 64: pick(std::integral_constant<int, 64>{}); break;
+    default: pick(std::integral_constant<int, 128>{}); break;
+  }
   return hipGetLastError();
 }
 

@@ -61,7 +61,7 @@ __global__ __launch_bounds__(512) void delta_grads_kernel(DeltaArgs a) {
     const float* F = a.F + kh * C * P;
     const brsrc ro = make_rsrc((const char*)a.dout + ((int64_t)start * a.H + h) * P * ES,
                                (uint32_t)(len - 1) * vrow + P * ES);
-    if (tid < 3 * C) gl[tid] = a.gates[kh * (3 * C) + tid];
+    if (tid < 3 * C) gl[tid] = a.gates[kh * kDeltaGates + tid];
     f32x4 dq[TH], dr[TH], dw[TH], cc[4];
 #pragma unroll
     for (int i = 0; i < TH; ++i) dq[i] = dr[i] = dw[i] = zero;

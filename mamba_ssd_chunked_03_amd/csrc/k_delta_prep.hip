@@ -1,193 +1,299 @@
-// Gated delta rule, per chunk of 64 tokens and head: the running decay, and the chunk
-// matrices R = M (I + diag(b) M)^-1 with M = strict lower (K K^T . D), and
-// P = scale Q K^T . D (lower), plane-split and in the order MFMA operand loads read.
+// Gated delta rule, bf16 io, per chunk of 64 tokens and head: the running decay, and the
+// chunk matrices R = M (I + diag(b) M)^-1 with M = strict lower (K K^T . D), and
+// P = scale Q K^T . D (lower), as bf16 planes in the order the chains' operands take.
 //
-// A workgroup takes one chunk and up to four heads of one group: its four waves form
-// K K^T and Q K^T once (MFMA, into LDS), then each wave solves one head's triangle by
-// forward substitution in fp32, row i of R from the rows above it,
-//   R_i = M_i - sum_{j<i} M_ij b_j R_j,
-// with a lane per column: it is backward stable whatever the keys (equal keys and
-// b = 1 leave entries that a product of powers of M would cancel to nothing).
+// One wave per (chunk, up to HPW heads of one group); waves do not interact.  K K^T and
+// Q K^T are computed transposed, so that a lane holds four (P: eight) consecutive
+// entries of a row: M is then an fp32 MFMA operand, and P a stored one, as it comes out.
+//
+// R by blocks of 16: the diagonal blocks by forward substitution in fp32, all four at
+// once (lane = block and column),  R_i = M_i - sum_{j<i} M_ij b_j R_j,  then
+//   Y_IJ = M_IJ - sum_{K=J}^{I-1} M_IK b_K R_KJ,   R_IJ = Y_IJ - R_II (b_I Y_IJ)
+// on the fp32 matrix cores, an accumulator tile being the next product's operand without
+// a move (row 4q + e of a tile is depth 4q + e of step e).  Substitution inside the
+// blocks keeps it backward stable whatever the keys: equal keys and b = 1 leave entries
+// that a product of powers of M would cancel to nothing.
+//
 // The running sums of g are taken in fp64 and kept as a high and a low fp32 part:
 // exponents are differences of them.
-#include "delta.hpp"
+#include "delta_reg.hpp"
 
 namespace ssd {
 
-constexpr int kMatLd = 68;  // row stride of the 64 x 64 fp32 matrices in LDS
+constexpr int kPrepLd = 68;               // row stride of the 64 x 64 fp32 matrix
 
-// rows R, columns 8q..8q+7 of column block S of an fp32 LDS matrix (transposed: of its
-// transpose) as planes, stored where block `blk` of each plane lies.
-template <int NP, bool TR>
-__device__ __forceinline__ void store_block(const float* m, uint16_t* dst, int blk, int R, int S, int lane) {
-  const int r = 16 * R + (lane & 15), c = 32 * S + 8 * (lane >> 4);
-  f32x4 a, b;
-  if constexpr (TR) {
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      a[e] = m[(c + e) * kMatLd + r];
-      b[e] = m[(c + 4 + e) * kMatLd + r];
-    }
-  } else {
-    a = *(const f32x4*)(m + r * kMatLd + c);
-    b = *(const f32x4*)(m + r * kMatLd + c + 4);
-  }
-  u32x4 o[NP];
-  split8<NP>(a, b, o);
-#pragma unroll
-  for (int i = 0; i < NP; ++i) *(u32x4*)(dst + i * kTriPlane + blk * 512 + lane * 8) = o[i];
-}
-
-template <int N, class IO>
-__global__ __launch_bounds__(256) void delta_prep_kernel(DeltaArgs a, int hsplit) {
-  constexpr int PI = IO::PI, PM = IO::PM, KS = (N + 31) / 32, ES = sizeof(typename IO::T);
-  __shared__ __align__(16) float mats[6][kDeltaChunk * kMatLd];
-  float* KK = mats[4];
-  float* QK = mats[5];
+template <int N, bool SAVE>
+__global__ __launch_bounds__(256) void delta_prep_kernel(DeltaArgs a, int hpw, int64_t items) {
+  constexpr int KS = (N + 31) / 32, C = kDeltaChunk;
+  __shared__ __align__(16) float lds[4][C * kPrepLd + 3 * C];
   const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63, q = lane >> 4, r = lane & 15;
-  const int wg = xcd_order(blockIdx.x, gridDim.x);
-  const int hs = wg % hsplit, grp = (wg / hsplit) % a.G, ck = wg / hsplit / a.G;
+  float *Rm = lds[w], *gh = Rm + C * kPrepLd, *gl = gh + C, *bb = gl + C;
+  const int per = a.H / a.G, parts = (per + hpw - 1) / hpw;
+  const int64_t item = (int64_t)xcd_order(blockIdx.x, gridDim.x) * 4 + w;
+  if (item >= items) return;
+  const int part = (int)(item % parts), grp = (int)(item / parts % a.G), ck = (int)(item / parts / a.G);
   ChunkInfo ci = chunk_info(a.map, ck);
-  ci.start = __builtin_amdgcn_readfirstlane(ci.start);
-  ci.len = __builtin_amdgcn_readfirstlane(ci.len);
-  if (ci.len <= 0) return;  // an unused slot
-  const int per = a.H / a.G, h = grp * per + hs * 4 + w;
-  const bool mine = hs * 4 + w < per;
+  const int start = __builtin_amdgcn_readfirstlane(ci.start), len = __builtin_amdgcn_readfirstlane(ci.len);
+  if (len <= 0) return;  // an unused slot
+  const f32x4 zero = {0.f, 0.f, 0.f, 0.f};
 
-  // K K^T and Q K^T, lower block triangle: wave w rows 16w..16w+15
+  const uint32_t row = (uint32_t)a.G * N * 2;
+  const int64_t base = ((int64_t)start * a.G + grp) * N * 2;
+  const uint32_t span = (uint32_t)(len - 1) * row + N * 2;
+  const brsrc rk = make_rsrc((const char*)a.k + base, span), rq = make_rsrc((const char*)a.q + base, span);
+  auto frag = [&](brsrc rs, int t, int ks) {
+    return as_bf16x8(buf_load16(rs, 32 * ks + 8 * q < N ? t * row + (32 * ks + 8 * q) * 2 : kNoOffset));
+  };
+  // K K^T, 16 x 16 blocks J <= I: lane (q, r) row 16I + r, columns 16J + 4q + e
+  f32x4 kk[4][4];
   {
-    const uint32_t row = (uint32_t)a.G * N * ES;
-    const int64_t base = ((int64_t)ci.start * a.G + grp) * N * ES;
-    const uint32_t span = (uint32_t)(ci.len - 1) * row + N * ES;
-    const brsrc rk = make_rsrc((const char*)a.k + base, span), rq = make_rsrc((const char*)a.q + base, span);
-    auto frag = [&](brsrc rs, int R, int ks) {
-      Raw8<IO> x;
-      x.load(rs, 32 * ks + 8 * q < N ? (16 * R + r) * row + (32 * ks + 8 * q) * ES : kNoOffset);
-      return raw_planes<IO>(x);
-    };
-    Planes<PI> kf[KS], qf[KS];
+    bf16x8 kf[4][KS];
 #pragma unroll
-    for (int ks = 0; ks < KS; ++ks) {
-      kf[ks] = frag(rk, w, ks);
-      qf[ks] = frag(rq, w, ks);
-    }
-    for (int J = 0; J <= w; ++J) {
-      f32x4 kk = {0.f, 0.f, 0.f, 0.f}, qk = kk;
+    for (int I = 0; I < 4; ++I)
 #pragma unroll
-      for (int ks = 0; ks < KS; ++ks) {
-        const Planes<PI> jf = frag(rk, J, ks);
-        kk = mma<PM>(kf[ks], jf, kk);
-        qk = mma<PM>(qf[ks], jf, qk);
+      for (int ks = 0; ks < KS; ++ks) kf[I][ks] = frag(rk, 16 * I + r, ks);
+#pragma unroll
+    for (int I = 0; I < 4; ++I)
+#pragma unroll
+      for (int J = 0; J <= I; ++J) {
+        kk[I][J] = zero;
+#pragma unroll
+        for (int ks = 0; ks < KS; ++ks) kk[I][J] = mfma_bf16(kf[J][ks], kf[I][ks], kk[I][J]);
       }
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        KK[(16 * w + 4 * q + e) * kMatLd + 16 * J + r] = kk[e];
-        QK[(16 * w + 4 * q + e) * kMatLd + 16 * J + r] = qk[e];
-      }
-    }
   }
-  __syncthreads();
-  if (!mine) return;
+  // Q K^T in the operands' row order.  qk[B][t][2S + u]: row 32B + row32(r, t), columns
+  // 32S + 8q + 4u + e; qt[S][u][2B + t] (for P^T): row 32S + row32(r, u), columns
+  // 32B + 8q + 4t + e
+  f32x4 qk[2][2][4], qt[2][2][4];
+  {
+    bf16x8 kf[2][2][KS], qf[2][2][KS];
+#pragma unroll
+    for (int B = 0; B < 2; ++B)
+#pragma unroll
+      for (int t = 0; t < 2; ++t)
+#pragma unroll
+        for (int ks = 0; ks < KS; ++ks) {
+          kf[B][t][ks] = frag(rk, 32 * B + row32(r, t), ks);
+          qf[B][t][ks] = frag(rq, 32 * B + row32(r, t), ks);
+        }
+#pragma unroll
+    for (int B = 0; B < 2; ++B)
+#pragma unroll
+      for (int S = 0; S <= B; ++S)
+#pragma unroll
+        for (int t = 0; t < 2; ++t)
+#pragma unroll
+          for (int u = 0; u < 2; ++u) {
+            qk[B][t][2 * S + u] = zero;
+#pragma unroll
+            for (int ks = 0; ks < KS; ++ks)
+              qk[B][t][2 * S + u] = mfma_bf16(kf[S][u][ks], qf[B][t][ks], qk[B][t][2 * S + u]);
+            if constexpr (SAVE) {
+              qt[S][u][2 * B + t] = zero;
+#pragma unroll
+              for (int ks = 0; ks < KS; ++ks)
+                qt[S][u][2 * B + t] = mfma_bf16(qf[B][t][ks], kf[S][u][ks], qt[S][u][2 * B + t]);
+            }
+          }
+  }
 
-  // gates: lane = token; past the chunk's end the decay stays and beta is zero
-  const int64_t tok = (int64_t)ci.start + lane;
-  const float gv = lane < ci.len ? fmaxf(a.g[tok * a.H + h], kDeltaMinGate) : 0.f;
-  const float bv = lane < ci.len ? a.beta[tok * a.H + h] : 0.f;
-  double G = (double)gv * 1.4426950408889634073599;
+  for (int hh = part * hpw; hh < min(per, (part + 1) * hpw); ++hh) {
+    const int h = grp * per + hh;
+    const int64_t kh = (int64_t)ck * a.H + h;
+    // gates: lane = token; past the chunk's end the decay stays and beta is zero
+    const int64_t tok = (int64_t)start + lane;
+    const float gv = lane < len ? fmaxf(a.g[tok * a.H + h], kDeltaMinGate) : 0.f;
+    const float bv = lane < len ? a.beta[tok * a.H + h] : 0.f;
+    double G = (double)gv * 1.4426950408889634073599;
 #pragma unroll
-  for (int d = 1; d < 64; d <<= 1) {
-    const double up = __shfl_up(G, d);
-    if (lane >= d) G += up;
-  }
-  const float Gh = (float)G, Gl = (float)(G - (double)Gh);
-  const int64_t kh = (int64_t)ck * a.H + h;
-  float* gt = a.gates + kh * (3 * kDeltaChunk);
-  gt[lane] = Gh;
-  gt[kDeltaChunk + lane] = Gl;
-  gt[2 * kDeltaChunk + lane] = bv;
-
-  float* M = mats[w];
-  // M (strict lower), lane = column
-#pragma unroll 8
-  for (int i = 0; i < kDeltaChunk; ++i) {
-    const float d = (__shfl(Gh, i) - Gh) + (__shfl(Gl, i) - Gl);
-    M[i * kMatLd + lane] = lane < i ? KK[i * kMatLd + lane] * exp2_fast(d) : 0.f;
-  }
-  __builtin_amdgcn_wave_barrier();
-  // forward substitution, row by row in place: br[j] = b_j R_j (this lane's column)
-  float br[kDeltaChunk];
-#pragma unroll
-  for (int i = 0; i < kDeltaChunk; ++i) {
-    float s[4] = {M[i * kMatLd + lane], 0.f, 0.f, 0.f};
-#pragma unroll
-    for (int j4 = 0; j4 < (i + 3) / 4; ++j4) {
-      const f32x4 m = *(const f32x4*)(M + i * kMatLd + 4 * j4);  // one address: a broadcast
-#pragma unroll
-      for (int e = 0; e < 4; ++e)
-        if (4 * j4 + e < i) s[e] -= m[e] * br[4 * j4 + e];
+    for (int d = 1; d < 64; d <<= 1) {
+      const double up = __shfl_up(G, d);
+      if (lane >= d) G += up;
     }
-    const float x = (s[0] + s[1]) + (s[2] + s[3]);
+    const float Gh = (float)G, Gl = (float)(G - (double)Gh);
+    const float Ch = wave_last(Gh), Cl = wave_last(Gl);
+    float* gt = a.gates + kh * kDeltaGates;
+    gt[lane] = Gh;
+    gt[C + lane] = Gl;
+    gt[2 * C + lane] = bv;
+    gt[3 * C + lane] = exp2_hl(Gh, Gl);
+    gt[4 * C + lane] = exp2_fast((Ch - Gh) + (Cl - Gl));
     __builtin_amdgcn_wave_barrier();
-    M[i * kMatLd + lane] = x;
-    br[i] = x * __int_as_float(__builtin_amdgcn_readlane(__float_as_int(bv), i));
-  }
-  __builtin_amdgcn_wave_barrier();
-  {
-    uint16_t* dst = a.R + kh * (PM * kTriPlane);
+    gh[lane] = Gh;
+    gl[lane] = Gl;
+    bb[lane] = bv;
+    __builtin_amdgcn_wave_barrier();
+
+    // M, and its diagonal blocks in LDS where R's will be
+    f32x4 m[4][4];
 #pragma unroll
-    for (int R = 0; R < 4; ++R)
+    for (int I = 0; I < 4; ++I) {
+      const float hi = gh[16 * I + r], li = gl[16 * I + r];
 #pragma unroll
-      for (int S = 0; S <= (R >= 2); ++S) store_block<PM, false>(M, dst, tri_block(R, S), R, S, lane);
-    if (a.Rt) {
-      dst = a.Rt + kh * (PM * kTriPlane);
+      for (int J = 0; J <= I; ++J) {
+        const f32x4 hj = *(const f32x4*)(gh + 16 * J + 4 * q), lj = *(const f32x4*)(gl + 16 * J + 4 * q);
 #pragma unroll
-      for (int R = 0; R < 4; ++R)
-#pragma unroll
-        for (int S = R >= 2; S < 2; ++S) store_block<PM, true>(M, dst, trit_block(R, S), R, S, lane);
+        for (int e = 0; e < 4; ++e) {
+          const float d = exp2_fast((hi - hj[e]) + (li - lj[e]));
+          m[I][J][e] = J < I || 4 * q + e < r ? kk[I][J][e] * d : 0.f;
+        }
+      }
+      *(f32x4*)(Rm + (16 * I + r) * kPrepLd + 16 * I + 4 * q) = m[I][I];
     }
-  }
-  __builtin_amdgcn_wave_barrier();
-  // P over the same buffer (inclusive lower triangle)
-#pragma unroll 8
-  for (int i = 0; i < kDeltaChunk; ++i) {
-    const float d = (__shfl(Gh, i) - Gh) + (__shfl(Gl, i) - Gl);
-    M[i * kMatLd + lane] = lane <= i ? a.scale * (QK[i * kMatLd + lane] * exp2_fast(d)) : 0.f;
-  }
-  __builtin_amdgcn_wave_barrier();
-  {
-    constexpr int PF = PI;  // planes of P that the output takes (bf16 outputs: one)
-    uint16_t* dst = a.Pm + kh * (PF * kTriPlane);
+    __builtin_amdgcn_wave_barrier();
+    // diagonal blocks: lane (q, r) column r of block q; row i of R takes the place of row i
+    // of M, which no later row reads
+    {
+      float* mb = Rm + 16 * q * kPrepLd + 16 * q;
+      float br[16];
 #pragma unroll
-    for (int R = 0; R < 4; ++R)
+      for (int i = 0; i < 16; ++i) {
+        float s[2] = {mb[i * kPrepLd + r], 0.f};
 #pragma unroll
-      for (int S = 0; S <= (R >= 2); ++S) store_block<PF, false>(M, dst, tri_block(R, S), R, S, lane);
-    if (a.Pt) {
-      dst = a.Pt + kh * (PM * kTriPlane);
+        for (int j4 = 0; j4 < (i + 3) / 4; ++j4) {
+          const f32x4 x = *(const f32x4*)(mb + i * kPrepLd + 4 * j4);
 #pragma unroll
-      for (int R = 0; R < 4; ++R)
+          for (int e = 0; e < 4; ++e)
+            if (4 * j4 + e < i) s[e & 1] -= x[e] * br[4 * j4 + e];
+        }
+        const float x = s[0] + s[1];
+        __builtin_amdgcn_wave_barrier();
+        mb[i * kPrepLd + r] = x;
+        br[i] = bb[16 * q + i] * x;
+      }
+      // the blocks right of the first and third diagonal ones are read with them
 #pragma unroll
-        for (int S = R >= 2; S < 2; ++S) store_block<PM, true>(M, dst, trit_block(R, S), R, S, lane);
+      for (int B = 0; B < 2; ++B)
+        *(f32x4*)(Rm + (32 * B + r) * kPrepLd + 32 * B + 16 + 4 * q) = zero;
+    }
+    __builtin_amdgcn_wave_barrier();
+    // the blocks below, column by column: br[K] = b_K R_KJ (K = J: minus the identity)
+#pragma unroll
+    for (int J = 0; J < 3; ++J) {
+      f32x4 br[4];
+      {
+        const f32x4 b = *(const f32x4*)(bb + 16 * J + 4 * q);
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          br[J][e] = b[e] * Rm[(16 * J + 4 * q + e) * kPrepLd + 16 * J + r] - (4 * q + e == r ? 1.f : 0.f);
+      }
+#pragma unroll
+      for (int I = J + 1; I < 4; ++I) {
+        f32x4 y = zero;
+#pragma unroll
+        for (int K = J; K < I; ++K)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) y = mfma_f32(m[I][K][e], br[K][e], y);
+        y = -y;
+        const f32x4 b = *(const f32x4*)(bb + 16 * I + 4 * q);
+        const f32x4 rd = *(const f32x4*)(Rm + (16 * I + r) * kPrepLd + 16 * I + 4 * q);
+        const f32x4 by = b * y;
+        f32x4 x = zero;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) x = mfma_f32(rd[e], by[e], x);
+        x = y - x;
+        br[I] = b * x;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) Rm[(16 * I + 4 * q + e) * kPrepLd + 16 * J + r] = x[e];
+      }
+    }
+    __builtin_amdgcn_wave_barrier();
+    {
+      uint16_t* dst = a.R + kh * (2 * kTriPlane) + lane * 8;
+      uint16_t* dt = SAVE ? a.Rt + kh * (2 * kTriPlane) + lane * 8 : nullptr;
+#pragma unroll
+      for (int B = 0; B < 2; ++B)
+#pragma unroll
+        for (int S = 0; S <= B; ++S)
+#pragma unroll
+          for (int t = 0; t < 2; ++t) {
+            const float* src = Rm + (32 * B + row32(r, t)) * kPrepLd + 32 * S + 8 * q;
+            u32x4 o[2];
+            split8<2>(*(const f32x4*)src, *(const f32x4*)(src + 4), o);
+#pragma unroll
+            for (int i = 0; i < 2; ++i) *(u32x4*)(dst + i * kTriPlane + low_block(B, t, S) * 512) = o[i];
+            if constexpr (SAVE) {
+              src = Rm + (32 * B + 8 * q) * kPrepLd + 32 * S + row32(r, t);
+              f32x4 x, y;
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                x[e] = src[e * kPrepLd];
+                y[e] = src[(e + 4) * kPrepLd];
+              }
+              split8<2>(x, y, o);
+#pragma unroll
+              for (int i = 0; i < 2; ++i) *(u32x4*)(dt + i * kTriPlane + up_block(S, t, B) * 512) = o[i];
+            }
+          }
+    }
+    // P and its transpose
+    {
+      uint16_t* dst = a.Pm + kh * kTriPlane + lane * 8;
+      uint16_t* dt = SAVE ? a.Pt + kh * (2 * kTriPlane) + lane * 8 : nullptr;
+#pragma unroll
+      for (int B = 0; B < 2; ++B)
+#pragma unroll
+        for (int S = 0; S <= B; ++S)
+#pragma unroll
+          for (int t = 0; t < 2; ++t) {
+            const int ro = row32(r, t);
+            f32x4 v[2];
+            {
+              const float hi = gh[32 * B + ro], li = gl[32 * B + ro];
+#pragma unroll
+              for (int u = 0; u < 2; ++u) {
+                const int c = 8 * q + 4 * u;
+                const f32x4 hj = *(const f32x4*)(gh + 32 * S + c), lj = *(const f32x4*)(gl + 32 * S + c);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                  const float d = exp2_fast((hi - hj[e]) + (li - lj[e]));
+                  v[u][e] = S < B || c + e <= ro ? a.scale * (qk[B][t][2 * S + u][e] * d) : 0.f;
+                }
+              }
+              u32x4 o[1];
+              split8<1>(v[0], v[1], o);
+              *(u32x4*)(dst + low_block(B, t, S) * 512) = o[0];
+            }
+            if constexpr (SAVE) {
+              const float hj = gh[32 * S + ro], lj = gl[32 * S + ro];
+#pragma unroll
+              for (int u = 0; u < 2; ++u) {
+                const int c = 8 * q + 4 * u;
+                const f32x4 hi = *(const f32x4*)(gh + 32 * B + c), li = *(const f32x4*)(gl + 32 * B + c);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                  const float d = exp2_fast((hi[e] - hj) + (li[e] - lj));
+                  v[u][e] = S < B || c + e >= ro ? a.scale * (qt[S][t][2 * B + u][e] * d) : 0.f;
+                }
+              }
+              u32x4 o[2];
+              split8<2>(v[0], v[1], o);
+#pragma unroll
+              for (int i = 0; i < 2; ++i) *(u32x4*)(dt + i * kTriPlane + up_block(S, t, B) * 512) = o[i];
+            }
+          }
     }
   }
 }
 
 hipError_t launch_delta_prep(const DeltaProb& p, const DeltaArgs& a, hipStream_t st) {
+  if (!p.io) return launch_delta_f32_prep(p, a, st);
   if (p.nck == 0) return hipSuccess;
-  const int hsplit = (p.H / p.G + 3) / 4;
-  const dim3 grid((unsigned)(p.nck * p.G * hsplit)), block(256);
-  auto go = [&](auto io) {
-    using IO = decltype(io);
-    switch (p.N) {
-      case 16: hipLaunchKernelGGL((delta_prep_kernel<16, IO>), grid, block, 0, st, a, hsplit); break;
-      case 32: hipLaunchKernelGGL((delta_prep_kernel<32, IO>), grid, block, 0, st, a, hsplit); break;
-      case 64: hipLaunchKernelGGL((delta_prep_kernel<64, IO>), grid, block, 0, st, a, hsplit); break;
-      default: hipLaunchKernelGGL((delta_prep_kernel<128, IO>), grid, block, 0, st, a, hsplit); break;
-    }
+  const int per = p.H / p.G, hpw = per >= 2 && p.nck * p.H >= 8192 ? 2 : 1;
+  const int64_t items = p.nck * p.G * ((per + hpw - 1) / hpw);
+  const dim3 grid((unsigned)((items + 3) / 4)), block(256);
+  auto go = [&](auto n) {
+    if (a.Rt)
+      hipLaunchKernelGGL((delta_prep_kernel<decltype(n)::value, true>), grid, block, 0, st, a, hpw, items);
+    else
+      hipLaunchKernelGGL((delta_prep_kernel<decltype(n)::value, false>), grid, block, 0, st, a, hpw, items);
   };
-  if (p.io)
-    go(IoBf16{});
-  else
-    go(IoF32{});
+  switch (p.N) {
+    case 16: go(std::integral_constant<int, 16>{}); break;
+    case 32: go(std::integral_constant<int, 32>{}); break;
+    case 64: go(std::integral_constant<int, 64>{}); break;
+    default: go(std::integral_constant<int, 128>{}); break;
+  }
   return hipGetLastError();
 }
 
