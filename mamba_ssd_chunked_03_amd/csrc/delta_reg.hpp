@@ -22,14 +22,28 @@ __device__ __forceinline__ int row32(int r, int t) { return 8 * (r >> 2) + 4 * t
 __host__ __device__ __forceinline__ int low_block(int B, int t, int S) { return B == 0 ? t : 2 + 2 * t + S; }
 __host__ __device__ __forceinline__ int up_block(int S, int t, int B) { return S == 1 ? 4 + t : 2 * t + B; }
 
-// Operand from an LDS tile stored [k][col] (row stride ld): depths k = 8q..8q+7, operand
-// row 4g + e <-> column 8g + 4t + e (t the tile of a 32-column block).  `p` points at
-// [k0][col0].
-__device__ __forceinline__ bf16x8 cols32(const uint16_t* tile, int ld, int t, int lane) {
+// LDS tile of 64 token rows of NP bf16 (NP = 32, 64, 128): rows 16 dwords apart modulo the
+// 64 banks, and shifted by four dwords every eight rows.  The 16 rows of an operand read
+// (row32) then fill the banks once, and the transposing reads take twice their minimum.
+template <int NP>
+struct TokTile {
+  static constexpr int LD = NP == 128 ? 160 : NP == 64 ? 96 : 32, SIZE = kDeltaChunk * LD + 64;
+  static __device__ __forceinline__ int at(int row, int col) { return row * LD + 8 * (row >> 3) + col; }
+};
+
+// Operand of depth 32 from such a tile: rows row0 + row32(r, t), depths col0 + 8q..8q+7.
+template <int NP>
+__device__ __forceinline__ bf16x8 tok_rows(const uint16_t* p, int row0, int t, int col0, int lane) {
+  return as_bf16x8(*(const u32x4*)(p + TokTile<NP>::at(row0 + row32(lane & 15, t), col0 + 8 * (lane >> 4))));
+}
+// ... the contraction along the rows: depths row0 + 8q..8q+7, operand row 4g + e <-> column
+// col0 + 8g + 4t + e, by transposing reads.
+template <int NP>
+__device__ __forceinline__ bf16x8 tok_cols(const uint16_t* tile, int row0, int t, int col0, int lane) {
   const int j = lane & 15;
-  const uint16_t* p = tile + (8 * (lane >> 4) + (j >> 2)) * ld + 8 * (j & 3) + 4 * t;
+  const uint16_t* p = tile + TokTile<NP>::at(row0 + 8 * (lane >> 4), col0 + 8 * (j & 3) + 4 * t) + (j >> 2) * TokTile<NP>::LD;
   v4i16 a = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4i16*)p);
-  v4i16 b = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4i16*)(p + 4 * ld));
+  v4i16 b = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_v4i16*)(p + 4 * TokTile<NP>::LD));
   v8i16 c = __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7);
   return __builtin_bit_cast(bf16x8, c);
 }
@@ -43,20 +57,6 @@ __device__ __forceinline__ Planes<NP> tile_planes(f32x4 a, f32x4 b) {
 #pragma unroll
   for (int i = 0; i < NP; ++i) f.p[i] = as_bf16x8(o[i]);
   return f;
-}
-
-// acc += a (one plane) times every plane of b, and the other way round (transposed tile)
-template <int NP>
-__device__ __forceinline__ f32x4 mma1(bf16x8 a, const Planes<NP>& b, f32x4 c) {
-#pragma unroll
-  for (int i = NP - 1; i >= 0; --i) c = mfma_bf16(a, b.p[i], c);
-  return c;
-}
-template <int NP>
-__device__ __forceinline__ f32x4 mma1t(const Planes<NP>& a, bf16x8 b, f32x4 c) {
-#pragma unroll
-  for (int i = NP - 1; i >= 0; --i) c = mfma_bf16(a.p[i], b, c);
-  return c;
 }
 
 }  // namespace ssd

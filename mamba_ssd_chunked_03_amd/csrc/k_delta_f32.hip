@@ -350,7 +350,9 @@ __global__ __launch_bounds__(256) void delta_f32_fwd_kernel(DeltaArgs a) {
       z = mma<PM>(lds_cols<PM>(Xl + 16 * t, LX, XPLANE, lane), Rf[0], z);
       if (w >= 2) z = mma<PM>(lds_cols<PM>(Xl + 32 * LX + 16 * t, LX, XPLANE, lane), Rf[1], z);
       z = X[t] - z;
-      if constexpr (SAVE) *(f32x4*)(a.Z + (kh * C + 16 * w + r) * a.P + p0 + 16 * t + 4 * q) = z;
+      if constexpr (SAVE)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) a.Z[(kh * a.P + p0 + 16 * t + 4 * q + e) * C + 16 * w + r] = z[e];
       uint2 o[PM];
       split4<PM>(b * z, o);
 #pragma unroll
@@ -592,7 +594,8 @@ __global__ __launch_bounds__(256) void delta_f32_bwd_kernel(DeltaArgs a) {
         f = mma<PM>(lds_cols<PM>(Xl + 32 * LX + 16 * t, LX, XPLANE, lane), Rf[1], f);
         if (w < 2) f = mma<PM>(lds_cols<PM>(Xl + 16 * t, LX, XPLANE, lane), Rf[0], f);
         f = E[t] - f;
-        *(f32x4*)(a.F + (kh * C + 16 * w + r) * a.P + p0 + 16 * t + 4 * q) = f;
+        #pragma unroll
+        for (int e = 0; e < 4; ++e) a.F[(kh * a.P + p0 + 16 * t + 4 * q + e) * C + 16 * w + r] = f[e];
         const f32x4 dx = b * f;
         store4io(rv, (16 * w + r) * vrow + (16 * t + 4 * q) * ES, dx, IO{});
         uint2 o[PM];

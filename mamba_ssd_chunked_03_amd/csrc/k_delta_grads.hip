@@ -26,14 +26,15 @@ __global__ __launch_bounds__(512) void delta_grads_kernel(DeltaArgs a) {
   constexpr int PI = IO::PI, PM = IO::PM, ES = sizeof(T), C = kDeltaChunk, NTH = 512;
   // columns of headdim staged at a time (the products' depth is 32; past P they are zero)
   constexpr int PB = P < 32 ? 32 : (P > (PM == 2 ? 64 : 32) ? (PM == 2 ? 64 : 32) : P), NB = (P + PB - 1) / PB;
-  constexpr int LN = N + 8, LP = PB + 8, LC = C + 8;
+  constexpr int LN = N + 8, LP = PB + 8, LC = C + 8;  // rows: dstate; headdim; tokens
   constexpr int TN = N / 16, TH = (TN + 1) / 2;  // column tiles, of one half
-  constexpr int SPL = PB * LN, TPL = C * LP, KPL = C * LN, CPL = C * LC;
-  constexpr int PH1 = 2 * PM * SPL + (2 * PM + PI) * TPL, PH2 = 2 * PI * KPL + 2 * PM * CPL;
+  constexpr int SPL = PB * LN, UPL = PB * LC, OPL = C * LP, KPL = C * LN, CPL = C * LC;
+  constexpr int PH1 = 2 * PM * SPL + 2 * PM * UPL + PI * OPL, PH2 = 2 * PI * KPL + 2 * PM * CPL;
   __shared__ __align__(16) uint16_t lds[PH1 > PH2 ? PH1 : PH2];
-  uint16_t *Sl = lds, *Dl = Sl + PM * SPL, *Ul = Dl + PM * SPL, *Xl = Ul + PM * TPL, *Ol = Xl + PM * TPL;
+  uint16_t *Sl = lds, *Dl = Sl + PM * SPL, *Ul = Dl + PM * SPL, *Xl = Ul + PM * UPL, *Ol = Xl + PM * UPL;
   uint16_t *Kl = lds, *Ql = Kl + PI * KPL, *Pl = Ql + PI * KPL, *Ml = Pl + PM * CPL;
-  __shared__ float gl[3 * C], red[2][2][C], sd[NTH / 64], bsum[C];
+  __shared__ __align__(16) float gl[3 * C];
+  __shared__ float red[2][2][C], sd[NTH / 64], bsum[NTH / 64][C];
 
   const int tid = threadIdx.x, w = __builtin_amdgcn_readfirstlane(tid >> 6), lane = tid & 63, q = lane >> 4, r = lane & 15;
   const int tb = w & 3, nh = w >> 2, tok = 16 * tb + r;
@@ -61,13 +62,15 @@ __global__ __launch_bounds__(512) void delta_grads_kernel(DeltaArgs a) {
     const float* F = a.F + kh * C * P;
     const brsrc ro = make_rsrc((const char*)a.dout + ((int64_t)start * a.H + h) * P * ES,
                                (uint32_t)(len - 1) * vrow + P * ES);
+    const brsrc rdv = make_rsrc((char*)a.dv + ((int64_t)start * a.H + h) * P * ES, (uint32_t)(len - 1) * vrow + P * ES);
     if (tid < 3 * C) gl[tid] = a.gates[kh * kDeltaGates + tid];
     f32x4 dq[TH], dr[TH], dw[TH], cc[4];
 #pragma unroll
     for (int i = 0; i < TH; ++i) dq[i] = dr[i] = dw[i] = zero;
 #pragma unroll
     for (int i = 0; i < 4; ++i) cc[i] = zero;
-    float sdot = 0.f, bdot = 0.f;
+    float sdot = 0.f;
+    f32x4 bdot[2] = {zero, zero};  // F . Z of eight tokens, this thread's rows
     __syncthreads();
 #pragma unroll 1
     for (int pb = 0; pb < NB; ++pb) {
@@ -90,38 +93,45 @@ __global__ __launch_bounds__(512) void delta_grads_kernel(DeltaArgs a) {
 #pragma unroll
         for (int m = 0; m < PM; ++m) *(uint2*)(Dl + m * SPL + row * LN + col) = o[m];
       }
-      constexpr int PCS = PB / 8, TE = C * PCS;  // 8-element pieces; those of a token are adjacent lanes
-      if (tid < TE) {
-        const int t = tid / PCS, col = (tid % PCS) * 8, p = pb * PB + col;
-        f32x4 z0 = zero, z1 = zero, f0 = zero, f1 = zero;
+      // Z and F (PB x 64, tokens fastest) as planes of U and dX, and dO (64 x PB)
+      if (tid < PB * C / 8) {
+        const int row = tid / (C / 8), p = pb * PB + row, t8 = (tid % (C / 8)) * 8;
+        f32x4 z[2] = {zero, zero}, f[2] = {zero, zero}, b[2];
         if (p < P) {
-          z0 = *(const f32x4*)(Z + t * P + p);
-          z1 = *(const f32x4*)(Z + t * P + p + 4);
-          f0 = *(const f32x4*)(F + t * P + p);
-          f1 = *(const f32x4*)(F + t * P + p + 4);
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            z[i] = *(const f32x4*)(Z + p * C + t8 + 4 * i);
+            f[i] = *(const f32x4*)(F + p * C + t8 + 4 * i);
+          }
         }
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          b[i] = *(const f32x4*)(gl + 2 * C + t8 + 4 * i);
+          bdot[i] += z[i] * f[i];
+        }
+        u32x4 o[PM];
+        split8<PM>(b[0] * z[0], b[1] * z[1], o);
+#pragma unroll
+        for (int m = 0; m < PM; ++m) *(u32x4*)(Ul + m * UPL + row * LC + t8) = o[m];
+        split8<PM>(b[0] * f[0], b[1] * f[1], o);
+#pragma unroll
+        for (int m = 0; m < PM; ++m) *(u32x4*)(Xl + m * UPL + row * LC + t8) = o[m];
+      }
+      if (tid < C * PB / 8) {
+        const int t = tid / (PB / 8), col = (tid % (PB / 8)) * 8, p = pb * PB + col;
         Raw8<IO> o8;
         o8.load(ro, p < P ? t * vrow + p * ES : kNoOffset);
-        const float b = gl[2 * C + t];
-        bdot += (z0[0] * f0[0] + z0[1] * f0[1] + z0[2] * f0[2] + z0[3] * f0[3]) +
-                (z1[0] * f1[0] + z1[1] * f1[1] + z1[2] * f1[2] + z1[3] * f1[3]);
-        u32x4 o[PM], oo[PI];
-        split8<PM>(b * z0, b * z1, o);
+        u32x4 o[PI];
+        o8.planes(o);
 #pragma unroll
-        for (int m = 0; m < PM; ++m) *(u32x4*)(Ul + m * TPL + t * LP + col) = o[m];
-        split8<PM>(b * f0, b * f1, o);
-#pragma unroll
-        for (int m = 0; m < PM; ++m) *(u32x4*)(Xl + m * TPL + t * LP + col) = o[m];
-        o8.planes(oo);
-#pragma unroll
-        for (int m = 0; m < PI; ++m) *(u32x4*)(Ol + m * TPL + t * LP + col) = oo[m];
+        for (int m = 0; m < PI; ++m) *(u32x4*)(Ol + m * OPL + t * LP + col) = o[m];
       }
       __syncthreads();
 #pragma unroll 1
       for (int ks = 0; ks < PB / 32; ++ks) {
-        const Planes<PI> of = lds_rows<PI>(Ol + 16 * tb * LP + 32 * ks, LP, TPL, lane);
-        const Planes<PM> xf = lds_rows<PM>(Xl + 16 * tb * LP + 32 * ks, LP, TPL, lane);
-        const Planes<PM> uf = lds_rows<PM>(Ul + 16 * tb * LP + 32 * ks, LP, TPL, lane);
+        const Planes<PI> of = lds_rows<PI>(Ol + 16 * tb * LP + 32 * ks, LP, OPL, lane);
+        const Planes<PM> xf = lds_cols<PM>(Xl + 32 * ks * LC + 16 * tb, LC, UPL, lane);
+        const Planes<PM> uf = lds_cols<PM>(Ul + 32 * ks * LC + 16 * tb, LC, UPL, lane);
 #pragma unroll
         for (int i = 0; i < TH; ++i) {
           const int nt = nh * TH + i;
@@ -132,11 +142,15 @@ __global__ __launch_bounds__(512) void delta_grads_kernel(DeltaArgs a) {
             dw[i] = mma<PM>(lds_cols<PM>(Dl + 32 * ks * LN + 16 * nt, LN, SPL, lane), uf, dw[i]);
           }
         }
+        // dX rounded to bf16 is its first plane: dV (the fp32 chain stores its own)
+        if constexpr (PI == 1)
+          if (nh == 0 && pb * PB + 32 * ks + 8 * q < P)
+            buf_store16(rdv, tok * vrow + (pb * PB + 32 * ks + 8 * q) * ES, __builtin_bit_cast(u32x4, xf.p[0]));
         // rows j (block J), columns i: the first half dO U^T, the second dX U^T
 #pragma unroll
         for (int J = 0; J < 4; ++J)
           if (J <= tb) {
-            const Planes<PM> jf = lds_rows<PM>(Ul + 16 * J * LP + 32 * ks, LP, TPL, lane);
+            const Planes<PM> jf = lds_cols<PM>(Ul + 32 * ks * LC + 16 * J, LC, UPL, lane);
             cc[J] = nh == 0 ? mma<PM>(jf, of, cc[J]) : mma<PM>(jf, xf, cc[J]);
           }
       }
@@ -230,12 +244,17 @@ __global__ __launch_bounds__(512) void delta_grads_kernel(DeltaArgs a) {
     }
     sdot = wave_sum(sdot);
     if (lane == 0) sd[w] = sdot;
-    {
-      constexpr int PCS = PB / 8;
+    // F . Z over the rows of a wave (lanes eight apart), in order over the waves below
 #pragma unroll
-      for (int m = 1; m < PCS; m <<= 1) bdot += __shfl_xor(bdot, m);
-      if (tid < C * PCS && tid % PCS == 0) bsum[tid / PCS] = bdot;
-    }
+    for (int i = 0; i < 2; ++i)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        float v = bdot[i][e];
+        v += __shfl_xor(v, 8);
+        v += __shfl_xor(v, 16);
+        v += __shfl_xor(v, 32);
+        if (lane < 8) bsum[w][lane * 8 + 4 * i + e] = v;
+      }
     __syncthreads();
     if (w == 0) {
       double x = (double)red[0][0][lane] + (double)red[0][1][lane];
@@ -255,7 +274,9 @@ __global__ __launch_bounds__(512) void delta_grads_kernel(DeltaArgs a) {
       if (lane < len) {
         const int64_t at = ((int64_t)start + lane) * a.H + h;
         a.dg[at] = (float)(x + (y - wj));
-        a.dbeta[at] = bsum[lane];
+        float v = bsum[0][lane];
+        for (int i = 1; i < NTH / 64; ++i) v += bsum[i][lane];
+        a.dbeta[at] = v;
       }
     }
     // (the next head's first barrier is behind these reads: gl is rewritten before it)
