@@ -71,7 +71,7 @@ DeltaLayout delta_layout(const DeltaProb& p) {
   DeltaLayout l;
   std::memset(&l, 0, sizeof(l));
   if (p.nck == 0 && !p.packed) return l;
-  const size_t ch = (size_t)p.nck * p.H, state = (size_t)p.P * p.N * 4, rows = (size_t)kDeltaChunk * p.P * 4;
+  const size_t ch = (size_t)p.nck * p.H, state = (size_t)p.P * state_cols(p.N) * 4, rows = (size_t)kDeltaChunk * p.P * 4;
   const size_t PM = p.io ? IoBf16::PM : IoF32::PM, PF = p.io ? IoBf16::PI : IoF32::PI;
   size_t o = 0;
   auto take = [&](size_t bytes) {

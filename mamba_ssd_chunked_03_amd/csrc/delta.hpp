@@ -59,11 +59,12 @@ struct DeltaArgs {
   float* final_states;
   float* gates;                // (nck, H, kDeltaGates): see below
   uint16_t *R, *Pm, *Rt, *Pt;  // plane-split chunk matrices in fragment order (null: not kept)
-  float *S, *Z;                // kept for the backward: states entering each chunk, Z
+  float *S, *Z;                // kept for the backward: states entering each chunk, Z (tile order)
   // backward
   const void* dout;
   const float* d_final;
-  float *dS, *F, *d_init;
+  float *dS, *F;               // adjoints of the states leaving each chunk, F (tile order)
+  float* d_init;
   void *dq, *dk, *dv;
   float *dg, *dbeta;
 };
@@ -71,6 +72,20 @@ struct DeltaArgs {
 // Per (chunk, head), 64 tokens each: running log2 decay G (high part, low part), beta; and
 // where io is bf16 exp(G), exp(G_C - G).  Past the chunk's end G stays and beta is zero.
 constexpr int kDeltaGates = 5 * kDeltaChunk;
+
+// States and their adjoints per (chunk, head), and Z and F, are kept in the order of the
+// chains' accumulator tiles, 16 columns of headdim after the other, so that a wave stores
+// 1 KB runs: states (P / 16, NP / 32, 2, 64 lanes, 4), NP = dstate or 32, lane 16 q + r of
+// tile (k, t) holding row r, columns 32k + 8q + 4t + 0..3; Z, F (P / 16, 4, 64 lanes, 4),
+// lane 16 q + r of tile i column r of tokens 32 (i / 2) + 8q + 4 (i % 2) + 0..3.
+__host__ __device__ __forceinline__ int state_cols(int N) { return N < 32 ? 32 : N; }
+// float offset of columns n..n+3 (n a multiple of 4) of headdim row p
+__device__ __forceinline__ int state_at(int p, int n, int NP) {
+  return ((((p >> 4) * (NP >> 5) + (n >> 5)) * 2 + ((n >> 2) & 1)) * 64 + ((n & 31) >> 3) * 16 + (p & 15)) * 4;
+}
+__device__ __forceinline__ int row_at(int p, int t) {
+  return (((p >> 4) * 4 + (t >> 5) * 2 + ((t >> 2) & 1)) * 64 + ((t & 31) >> 3) * 16 + (p & 15)) * 4 + (t & 3);
+}
 
 hipError_t launch_delta_f32_prep(const DeltaProb& p, const DeltaArgs& a, hipStream_t st);
 hipError_t launch_delta_f32_fwd(const DeltaProb& p, const DeltaArgs& a, hipStream_t st);
@@ -101,17 +116,30 @@ struct Planes {
   bf16x8 p[NP];
 };
 
+// x - h for each half h of the bf16 pair w and its own x, exactly: one v_dot2c_f32_bf16 with
+// (-1, 0) or (0, -1) instead of a shift or mask and a subtraction.  (The masks come from
+// registers the compiler cannot see into: as an inline constant it prints -1.0, which the
+// instruction takes as fp32, that is for the other half.  Exact over 4 million pairs of
+// random bits, subnormals included; an infinity makes its neighbour's rest a NaN.)
+__device__ __forceinline__ void sub_bf2(uint32_t w, float& x0, float& x1) {
+  uint32_t c0 = 0x0000bf80u, c1 = 0xbf800000u;
+  asm("" : "+s"(c0));
+  asm("" : "+s"(c1));
+  const bf16x2v h = __builtin_bit_cast(bf16x2v, w);
+  x0 = __builtin_amdgcn_fdot2_f32_bf16(h, __builtin_bit_cast(bf16x2v, c0), x0, false);
+  x1 = __builtin_amdgcn_fdot2_f32_bf16(h, __builtin_bit_cast(bf16x2v, c1), x1, false);
+}
+
 // planes of 4 floats, 8 bytes each (consecutive elements)
 template <int NP>
 __device__ __forceinline__ void split4(f32x4 x, uint2 (&o)[NP]) {
+  float f[4] = {x[0], x[1], x[2], x[3]};
 #pragma unroll
   for (int i = 0; i < NP; ++i) {
-    o[i] = make_uint2(pack_bf2(x[0], x[1]), pack_bf2(x[2], x[3]));
+    o[i] = make_uint2(pack_bf2(f[0], f[1]), pack_bf2(f[2], f[3]));
     if (i + 1 < NP) {
-      x[0] -= bf_lo(o[i].x);
-      x[1] -= bf_hi(o[i].x);
-      x[2] -= bf_lo(o[i].y);
-      x[3] -= bf_hi(o[i].y);
+      sub_bf2(o[i].x, f[0], f[1]);
+      sub_bf2(o[i].y, f[2], f[3]);
     }
   }
 }

@@ -59,4 +59,20 @@ __device__ __forceinline__ Planes<NP> tile_planes(f32x4 a, f32x4 b) {
   return f;
 }
 
+// (sequence, workgroup of the sequence) of a chain's workgroup: each XCD takes the same part
+// of every sequence's `per` workgroups (heads of one group share K and Q in its L2), so that
+// a long sequence among short ones is spread over all of them.
+__device__ __forceinline__ void chain_order(int per, int& s, int& i) {
+  const int wg = blockIdx.x;
+  if (per % kNumXcd == 0) {
+    const int part = per / kNumXcd, slot = wg / kNumXcd;
+    s = slot / part;
+    i = wg % kNumXcd * part + slot % part;
+  } else {
+    const int l = xcd_order(wg, gridDim.x);
+    s = l / per;
+    i = l % per;
+  }
+}
+
 }  // namespace ssd

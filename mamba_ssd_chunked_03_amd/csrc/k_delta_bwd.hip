@@ -8,8 +8,8 @@
 // F and the dS of every chunk are stored for k_delta_grads.hip, which forms the gradients
 // chunk by chunk.  Registers, waves and tiles as in k_delta_fwd.hip.  The helper waves form
 // what does not wait for dS a chunk ahead: E0 = P^T dO and T = (scale exp(G) dO)^T Q.
-//   interval A(c)  chain: K dS^T, E                 helpers: R, T(c), Q, P, dO(c - 1) to LDS
-//   interval B(c)  chain: R^T (b E), F, the new dS   helpers: K(c - 1) to LDS, E0, T of c - 1
+//   interval A(c)  chain: K dS^T, E                 helpers: T(c), Q, P, dO(c - 1) to LDS
+//   interval B(c)  chain: R^T (b E), F, the new dS   helpers: K, R(c - 1) to LDS, E0, T of c - 1
 // Two planes throughout (the error of dS is not a result: 3e-6 of the gradients).
 #include "delta_reg.hpp"
 
@@ -20,14 +20,15 @@ __global__ __launch_bounds__(64 * NPT + 256, 1) void delta_bwd_kernel(DeltaArgs 
   constexpr int C = kDeltaChunk, NP = N < 32 ? 32 : N, KS = NP / 32;
   using Tile = TokTile<NP>;
   constexpr int LV = 16 * NPT + 8, EV = C * LV, ER = 2 * kTriPlane;
-  __shared__ __align__(16) uint16_t Kl[2][Tile::SIZE], Ql[Tile::SIZE], Rl[ER], Pl[ER], Ol[EV];
+  __shared__ __align__(16) uint16_t Kl[2][Tile::SIZE], Ql[Tile::SIZE], Rl[2][ER], Pl[ER], Ol[EV];
   __shared__ __align__(16) float gl[2][3 * C];  // beta, exp(G), exp(G_C - G)
   __shared__ __align__(16) f32x4 Ex[NPT][4][64], Tx[NPT][KS][2][64];  // E0 and T, tile order
 
   const int tid = threadIdx.x, w = __builtin_amdgcn_readfirstlane(tid >> 6), lane = tid & 63, q = lane >> 4, r = lane & 15;
   const int np = (ptiles + NPT - 1) / NPT;
-  const int wg = xcd_order(blockIdx.x, gridDim.x);
-  const int pg = wg % np, h = (wg / np) % a.H, s = wg / np / a.H;
+  int s, wg;
+  chain_order(a.H * np, s, wg);
+  const int pg = wg % np, h = wg / np;
   const int p0 = pg * 16 * NPT;
   const int pw = 16 * min(NPT, ptiles - pg * NPT);
   const int grp = h / (a.H / a.G);
@@ -50,6 +51,8 @@ __global__ __launch_bounds__(64 * NPT + 256, 1) void delta_bwd_kernel(DeltaArgs 
     Planes<2> sf[KS];
 #pragma unroll
     for (int k = 0; k < KS; ++k) sf[k] = tile_planes<2>(S[k][0], S[k][1]);
+    f32x4* kS = (f32x4*)a.dS + (int64_t)(pc >> 4) * (KS * 2) * 64 + lane;  // of chunk slot 0
+    f32x4* kF = (f32x4*)a.F + (int64_t)(pc >> 4) * 4 * 64 + lane;
     __syncthreads();
     __syncthreads();
     for (int c = c1 - 1; c >= c0; --c) {
@@ -57,7 +60,10 @@ __global__ __launch_bounds__(64 * NPT + 256, 1) void delta_bwd_kernel(DeltaArgs 
       const float* g = gl[(c1 - 1 - c) & 1];
       const int64_t kh = (int64_t)c * a.H + h;
       // interval A: E, tile i = 2B + t with tokens 32B + 8q + 4t + e
-      f32x4 E[4], bt[4];
+      f32x4 E[4], bt[4], eg[4];
+      bf16x8 kt[KS][2];
+      Planes<2> Rf[6];
+      const float eC = g[C + C - 1];
       {
         bf16x8 kf[2][4];
         f32x4 ks[4];
@@ -83,10 +89,21 @@ __global__ __launch_bounds__(64 * NPT + 256, 1) void delta_bwd_kernel(DeltaArgs 
             for (int i = 0; i < 4; ++i) ks[i] = mfma_bf16(kf[k & 1][i], sf[k].p[m], ks[i]);
           if (live)
 #pragma unroll
-            for (int t = 0; t < 2; ++t)
-              if (scol(k, t) < N) *(f32x4*)(a.dS + (kh * a.P + pc) * N + scol(k, t)) = S[k][t];
+            for (int t = 0; t < 2; ++t) kS[(kh * (a.P / 16) * (KS * 2) + k * 2 + t) * 64] = S[k][t];
           __builtin_amdgcn_sched_barrier(0);
         }
+        // what the next interval starts with, under way while E is formed
+#pragma unroll
+        for (int i = 0; i < 6; ++i)
+#pragma unroll
+          for (int m = 0; m < 2; ++m)
+            Rf[i].p[m] = as_bf16x8(*(const u32x4*)(Rl[(c1 - 1 - c) & 1] + m * kTriPlane + i * 512 + lane * 8));
+#pragma unroll
+        for (int i = 0; i < 4; ++i) eg[i] = *(const f32x4*)(g + C + 32 * (i >> 1) + 8 * q + 4 * (i & 1));
+#pragma unroll
+        for (int k = 0; k < KS; ++k)
+#pragma unroll
+          for (int t = 0; t < 2; ++t) kt[k][t] = tok_cols<NP>(K, 0, t, 32 * k, lane);
 #pragma unroll
         for (int i = 0; i < 4; ++i)
           E[i] += *(const f32x4*)(g + 2 * C + 32 * (i >> 1) + 8 * q + 4 * (i & 1)) * ks[i];
@@ -96,36 +113,20 @@ __global__ __launch_bounds__(64 * NPT + 256, 1) void delta_bwd_kernel(DeltaArgs 
       for (int B = 0; B < 2; ++B) ef[B] = tile_planes<2>(bt[2 * B] * E[2 * B], bt[2 * B + 1] * E[2 * B + 1]);
       __syncthreads();
       // interval B: F = E - R^T (b E), by planes
-      f32x4 F[4], eg[4];
-      bf16x8 kt[KS][2];
-      const float eC = g[C + C - 1];
-      {
-        Planes<2> Rf[6];
+      f32x4 F[4];
 #pragma unroll
-        for (int i = 0; i < 6; ++i)
+      for (int i = 0; i < 4; ++i) F[i] = zero;
 #pragma unroll
-          for (int m = 0; m < 2; ++m) Rf[i].p[m] = as_bf16x8(*(const u32x4*)(Rl + m * kTriPlane + i * 512 + lane * 8));
+      for (int m = 0; m < 3; ++m)
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          eg[i] = *(const f32x4*)(g + C + 32 * (i >> 1) + 8 * q + 4 * (i & 1));
-          F[i] = zero;
-        }
+        for (int B2 = 1; B2 >= 0; --B2)
 #pragma unroll
-        for (int k = 0; k < KS; ++k)
+          for (int i = 0; i < (B2 ? 4 : 2); ++i)
+            F[i] = mfma_bf16(Rf[up_block(i >> 1, i & 1, B2)].p[m == 0], ef[B2].p[m == 1], F[i]);
 #pragma unroll
-          for (int t = 0; t < 2; ++t) {
-            S[k][t] = eC * S[k][t] + Tx[w][k][t][lane];
-            kt[k][t] = tok_cols<NP>(K, 0, t, 32 * k, lane);
-          }
-        __builtin_amdgcn_sched_barrier(0);
+      for (int k = 0; k < KS; ++k)
 #pragma unroll
-        for (int m = 0; m < 3; ++m)
-#pragma unroll
-          for (int B2 = 1; B2 >= 0; --B2)
-#pragma unroll
-            for (int i = 0; i < (B2 ? 4 : 2); ++i)
-              F[i] = mfma_bf16(Rf[up_block(i >> 1, i & 1, B2)].p[m == 0], ef[B2].p[m == 1], F[i]);
-      }
+        for (int t = 0; t < 2; ++t) S[k][t] = eC * S[k][t] + Tx[w][k][t][lane];
       Planes<2> wf[2];
 #pragma unroll
       for (int B = 0; B < 2; ++B) {
@@ -134,7 +135,7 @@ __global__ __launch_bounds__(64 * NPT + 256, 1) void delta_bwd_kernel(DeltaArgs 
         for (int t = 0; t < 2; ++t) {
           const int i = 2 * B + t;
           F[i] = E[i] - F[i];
-          if (live) *(f32x4*)(a.F + (kh * a.P + pc) * C + 32 * B + 8 * q + 4 * t) = F[i];
+          if (live) kF[(kh * (a.P / 16) * 4 + i) * 64] = F[i];
           wv[t] = -eg[i] * (bt[i] * F[i]);
         }
         wf[B] = tile_planes<2>(wv[0], wv[1]);
@@ -240,9 +241,9 @@ __global__ __launch_bounds__(64 * NPT + 256, 1) void delta_bwd_kernel(DeltaArgs 
       if (KX || e < C * N / 8) *(u32x4*)(Kl[buf] + Tile::at(e / (N / 8), (e % (N / 8)) * 8)) = xk[i];
     }
   };
-  auto put_r = [&]() {
+  auto put_r = [&](int buf) {
 #pragma unroll
-    for (int i = 0; i < RC; ++i) *(u32x4*)(Rl + (ht + i * 256) * 8) = xr[i];
+    for (int i = 0; i < RC; ++i) *(u32x4*)(Rl[buf] + (ht + i * 256) * 8) = xr[i];
   };
   auto put_ahead = [&](int buf) {  // what the helpers read, and the gates
 #pragma unroll
@@ -319,9 +320,11 @@ __global__ __launch_bounds__(64 * NPT + 256, 1) void delta_bwd_kernel(DeltaArgs 
     load_r(c1 - 1);
     put_ahead(0);
     put_k(0);
+    put_r(0);
     if (c1 - 2 >= c0) {
       load_ahead(c1 - 2);
       load_k(c1 - 2);
+      load_r(c1 - 2);
     }
   }
   __syncthreads();
@@ -330,7 +333,6 @@ __global__ __launch_bounds__(64 * NPT + 256, 1) void delta_bwd_kernel(DeltaArgs 
   for (int c = c1 - 1; c >= c0; --c) {
     const int nb = (c1 - c) & 1;  // the next chunk's buffer
     // interval A
-    put_r();
     if (works) {
 #pragma unroll
       for (int k = 0; k < KS; ++k)
@@ -338,7 +340,6 @@ __global__ __launch_bounds__(64 * NPT + 256, 1) void delta_bwd_kernel(DeltaArgs 
         for (int t = 0; t < 2; ++t) Tx[tile][k][t][lane] = T[k][t];
     }
     if (c > c0) {
-      load_r(c - 1);
       put_ahead(nb);
       if (c - 2 >= c0) load_ahead(c - 2);
     }
@@ -346,7 +347,11 @@ __global__ __launch_bounds__(64 * NPT + 256, 1) void delta_bwd_kernel(DeltaArgs 
     // interval B
     if (c > c0) {
       put_k(nb);
-      if (c - 2 >= c0) load_k(c - 2);
+      put_r(nb);
+      if (c - 2 >= c0) {
+        load_k(c - 2);
+        load_r(c - 2);
+      }
       ahead(nb);
     }
     __syncthreads();

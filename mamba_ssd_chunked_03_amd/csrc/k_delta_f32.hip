@@ -352,7 +352,7 @@ __global__ __launch_bounds__(256) void delta_f32_fwd_kernel(DeltaArgs a) {
       z = X[t] - z;
       if constexpr (SAVE)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) a.Z[(kh * a.P + p0 + 16 * t + 4 * q + e) * C + 16 * w + r] = z[e];
+        for (int e = 0; e < 4; ++e) a.Z[kh * a.P * C + row_at(p0 + 16 * t + 4 * q + e, 16 * w + r)] = z[e];
       uint2 o[PM];
       split4<PM>(b * z, o);
 #pragma unroll
@@ -373,7 +373,7 @@ __global__ __launch_bounds__(256) void delta_f32_fwd_kernel(DeltaArgs a) {
 #pragma unroll
         for (int t = 0; t < NT; ++t) {
           if constexpr (SAVE)
-            *(f32x4*)(a.S + (kh * a.P + p0 + 16 * t + r) * N + 16 * nt + 4 * q) = S[i][t];
+            *(f32x4*)(a.S + kh * a.P * NP + state_at(p0 + 16 * t + r, 16 * nt + 4 * q, NP)) = S[i][t];
           f32x4 acc = eC * S[i][t];
 #pragma unroll
           for (int S2 = 0; S2 < 2; ++S2)
@@ -595,7 +595,7 @@ __global__ __launch_bounds__(256) void delta_f32_bwd_kernel(DeltaArgs a) {
         if (w < 2) f = mma<PM>(lds_cols<PM>(Xl + 16 * t, LX, XPLANE, lane), Rf[0], f);
         f = E[t] - f;
         #pragma unroll
-        for (int e = 0; e < 4; ++e) a.F[(kh * a.P + p0 + 16 * t + 4 * q + e) * C + 16 * w + r] = f[e];
+        for (int e = 0; e < 4; ++e) a.F[kh * a.P * C + row_at(p0 + 16 * t + 4 * q + e, 16 * w + r)] = f[e];
         const f32x4 dx = b * f;
         store4io(rv, (16 * w + r) * vrow + (16 * t + 4 * q) * ES, dx, IO{});
         uint2 o[PM];
@@ -618,7 +618,7 @@ __global__ __launch_bounds__(256) void delta_f32_bwd_kernel(DeltaArgs a) {
         }
 #pragma unroll
         for (int t = 0; t < NT; ++t) {
-          *(f32x4*)(a.dS + (kh * a.P + p0 + 16 * t + r) * N + 16 * nt + 4 * q) = S[i][t];
+          *(f32x4*)(a.dS + kh * a.P * NP + state_at(p0 + 16 * t + r, 16 * nt + 4 * q, NP)) = S[i][t];
           f32x4 acc = eC * S[i][t];
 #pragma unroll
           for (int S2 = 0; S2 < 2; ++S2) {

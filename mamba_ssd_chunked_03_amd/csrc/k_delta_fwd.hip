@@ -11,8 +11,8 @@
 //   registers and copy them to LDS, and the first NPT of them form the output, one
 //   chunk's P U behind the chain, from the planes of S and U that the chain leaves in LDS.
 // Two barriers a chunk:
-//   interval A(c)  chain: K S^T, X                  helpers: R(c) to LDS, P U of c - 1, Q S^T of c
-//   interval B(c)  chain: R (b X), U, the new S     helpers: K, Q, V(c + 1), P(c) to LDS, next loads
+//   interval A(c)  chain: K S^T, X                  helpers: P(c - 1) to LDS, Q S^T of c
+//   interval B(c)  chain: R (b X), U, the new S     helpers: K, Q, R, V(c + 1) to LDS, O of c - 1
 // A compute unit takes in 50 KB a chunk whatever NPT is (58 KB with V and O at NPT = 4),
 // 1000 cycles of its load path at the least and 2000 when they come from HBM: issued by the
 // waves that compute, those loads held up everything behind them.
@@ -29,14 +29,15 @@ __global__ __launch_bounds__(64 * NPT + 256, 1) void delta_fwd_kernel(DeltaArgs 
   constexpr int C = kDeltaChunk, NP = N < 32 ? 32 : N, KS = NP / 32;
   using Tile = TokTile<NP>;
   constexpr int LV = 16 * NPT + 8, EV = C * LV, ER = 2 * kTriPlane, EP = kTriPlane;
-  __shared__ __align__(16) uint16_t Kl[2][Tile::SIZE], Ql[Tile::SIZE], Rl[ER], Pl[EP], Vl[EV];
+  __shared__ __align__(16) uint16_t Kl[2][Tile::SIZE], Ql[Tile::SIZE], Rl[2][ER], Pl[EP], Vl[EV];
   __shared__ __align__(16) float gl[2][3 * C];  // beta, exp(G), exp(G_C - G)
   __shared__ __align__(16) u32x4 Sx[NPT][KS][2][64], Ux[NPT][2][2][64];  // planes of S and U, operand order
 
   const int tid = threadIdx.x, w = __builtin_amdgcn_readfirstlane(tid >> 6), lane = tid & 63, q = lane >> 4, r = lane & 15;
   const int np = (ptiles + NPT - 1) / NPT;
-  const int wg = xcd_order(blockIdx.x, gridDim.x);
-  const int pg = wg % np, h = (wg / np) % a.H, s = wg / np / a.H;
+  int s, wg;
+  chain_order(a.H * np, s, wg);
+  const int pg = wg % np, h = wg / np;
   const int p0 = pg * 16 * NPT;                      // the workgroup's columns
   const int pw = 16 * min(NPT, ptiles - pg * NPT);   // (a last workgroup may have fewer)
   const int grp = h / (a.H / a.G);
@@ -66,6 +67,8 @@ __global__ __launch_bounds__(64 * NPT + 256, 1) void delta_fwd_kernel(DeltaArgs 
         for (int m = 0; m < 2; ++m) Sx[w][k][m][lane] = __builtin_bit_cast(u32x4, sf[k].p[m]);
       }
     };
+    f32x4* kS = (f32x4*)a.S + (int64_t)(pc >> 4) * (KS * 2) * 64 + lane;  // of chunk slot 0 (SAVE)
+    f32x4* kZ = (f32x4*)a.Z + (int64_t)(pc >> 4) * 4 * 64 + lane;
     put_state();
     __syncthreads();
     for (int c = c0; c < c1; ++c) {
@@ -101,11 +104,26 @@ __global__ __launch_bounds__(64 * NPT + 256, 1) void delta_fwd_kernel(DeltaArgs 
           if constexpr (SAVE)
             if (live)
 #pragma unroll
-              for (int t = 0; t < 2; ++t)
-                if (scol(k, t) < N) *(f32x4*)(a.S + (kh * a.P + pc) * N + scol(k, t)) = S[k][t];
+              for (int t = 0; t < 2; ++t) kS[(kh * (a.P / 16) * (KS * 2) + k * 2 + t) * 64] = S[k][t];
           __builtin_amdgcn_sched_barrier(0);
         }
       }
+      // what the next interval starts with, under way while X is formed
+      f32x4 er[4];
+      bf16x8 kt[KS][2];
+      Planes<2> Rf[6];
+#pragma unroll
+      for (int i = 0; i < 6; ++i)
+#pragma unroll
+        for (int m = 0; m < 2; ++m)
+          Rf[i].p[m] = as_bf16x8(*(const u32x4*)(Rl[(c - c0) & 1] + m * kTriPlane + i * 512 + lane * 8));
+#pragma unroll
+      for (int i = 0; i < 4; ++i) er[i] = *(const f32x4*)(g + 2 * C + 32 * (i >> 1) + 8 * q + 4 * (i & 1));
+      const float eC = g[C + C - 1];
+#pragma unroll
+      for (int k = 0; k < KS; ++k)
+#pragma unroll
+        for (int t = 0; t < 2; ++t) kt[k][t] = tok_cols<NP>(K, 0, t, 32 * k, lane);
       f32x4 X[4];
       Planes<2> xf[2];
 #pragma unroll
@@ -118,33 +136,20 @@ __global__ __launch_bounds__(64 * NPT + 256, 1) void delta_fwd_kernel(DeltaArgs 
       for (int B = 0; B < 2; ++B) xf[B] = tile_planes<2>(bt[2 * B] * X[2 * B], bt[2 * B + 1] * X[2 * B + 1]);
       __syncthreads();
       // interval B: Z = X - R (b X), by planes (low x high, high x low, high x high)
-      f32x4 Z[4], er[4];
-      bf16x8 kt[KS][2];
-      const float eC = g[C + C - 1];
-      {
-        Planes<2> Rf[6];
+      f32x4 Z[4];
 #pragma unroll
-        for (int i = 0; i < 6; ++i)
+      for (int i = 0; i < 4; ++i) Z[i] = zero;
 #pragma unroll
-          for (int m = 0; m < 2; ++m) Rf[i].p[m] = as_bf16x8(*(const u32x4*)(Rl + m * kTriPlane + i * 512 + lane * 8));
+      for (int m = 0; m < 3; ++m)
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          er[i] = *(const f32x4*)(g + 2 * C + 32 * (i >> 1) + 8 * q + 4 * (i & 1));
-          Z[i] = zero;
-        }
+        for (int S2 = 0; S2 < 2; ++S2)
 #pragma unroll
-        for (int k = 0; k < KS; ++k)
+          for (int i = 2 * S2; i < 4; ++i)
+            Z[i] = mfma_bf16(Rf[low_block(i >> 1, i & 1, S2)].p[m == 0], xf[S2].p[m == 1], Z[i]);
 #pragma unroll
-          for (int t = 0; t < 2; ++t) kt[k][t] = tok_cols<NP>(K, 0, t, 32 * k, lane);
-        __builtin_amdgcn_sched_barrier(0);
+      for (int k = 0; k < KS; ++k)
 #pragma unroll
-        for (int m = 0; m < 3; ++m)
-#pragma unroll
-          for (int S2 = 0; S2 < 2; ++S2)
-#pragma unroll
-            for (int i = 2 * S2; i < 4; ++i)
-              Z[i] = mfma_bf16(Rf[low_block(i >> 1, i & 1, S2)].p[m == 0], xf[S2].p[m == 1], Z[i]);
-      }
+        for (int t = 0; t < 2; ++t) S[k][t] = eC * S[k][t];
       Planes<3> wf[2];
 #pragma unroll
       for (int B = 0; B < 2; ++B) {
@@ -153,7 +158,7 @@ __global__ __launch_bounds__(64 * NPT + 256, 1) void delta_fwd_kernel(DeltaArgs 
           const int i = 2 * B + t;
           Z[i] = X[i] - Z[i];
           if constexpr (SAVE)
-            if (live) *(f32x4*)(a.Z + (kh * a.P + pc) * C + 32 * B + 8 * q + 4 * t) = Z[i];
+            if (live) kZ[(kh * (a.P / 16) * 4 + i) * 64] = Z[i];
           Z[i] = bt[i] * Z[i];
         }
         wf[B] = tile_planes<3>(er[2 * B] * Z[2 * B], er[2 * B + 1] * Z[2 * B + 1]);
@@ -162,10 +167,6 @@ __global__ __launch_bounds__(64 * NPT + 256, 1) void delta_fwd_kernel(DeltaArgs 
         for (int m = 0; m < 2; ++m) Ux[w][B][m][lane] = __builtin_bit_cast(u32x4, uf.p[m]);
       }
       // the state
-#pragma unroll
-      for (int k = 0; k < KS; ++k)
-#pragma unroll
-        for (int t = 0; t < 2; ++t) S[k][t] = eC * S[k][t];
 #pragma unroll
       for (int B = 0; B < 2; ++B) {
         bf16x8 kn[KS][2];
@@ -192,6 +193,7 @@ __global__ __launch_bounds__(64 * NPT + 256, 1) void delta_fwd_kernel(DeltaArgs 
       put_state();
       __syncthreads();
     }
+    __syncthreads();
     if (a.final_states && live) {
 #pragma unroll
       for (int k = 0; k < KS; ++k)
@@ -268,31 +270,45 @@ __global__ __launch_bounds__(64 * NPT + 256, 1) void delta_fwd_kernel(DeltaArgs 
     if (ht < 3 * C) gl[buf][ht] = xg;
   };
 
-  f32x4 qs[4];
-  // O of chunk c = what qs holds + P U, stored with rows headdim: four elements of a token a lane
-  auto finish = [&](int c) {
-    if (!outs) return;
-    bf16x8 pf[6];
-    Planes<2> uf[2];
+  auto put_r = [&](int buf) {
 #pragma unroll
-    for (int i = 0; i < 6; ++i) pf[i] = as_bf16x8(*(const u32x4*)(Pl + i * 512 + lane * 8));
+    for (int i = 0; i < RC; ++i) *(u32x4*)(Rl[buf] + (ht + i * 256) * 8) = xr[i];
+  };
+  auto put_p = [&]() {
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+      if ((ht + i * 256) * 8 < EP) *(u32x4*)(Pl + (ht + i * 256) * 8) = xp[i];
+  };
+
+  // qs: scale exp(G) (Q S^T)^T of the chunk last begun, qo of the one before it; uf: its U
+  f32x4 qs[4], qo[4];
+  Planes<2> uf[2];
+  auto take = [&]() {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) qo[i] = qs[i];
 #pragma unroll
     for (int B = 0; B < 2; ++B)
 #pragma unroll
       for (int m = 0; m < 2; ++m) uf[B].p[m] = as_bf16x8(Ux[tile][B][m][lane]);
+  };
+  // O of chunk c = qo + P U, stored with rows headdim: four elements of a token a lane
+  auto finish = [&](int c) {
+    bf16x8 pf[6];
+#pragma unroll
+    for (int i = 0; i < 6; ++i) pf[i] = as_bf16x8(*(const u32x4*)(Pl + i * 512 + lane * 8));
 #pragma unroll
     for (int m = 1; m >= 0; --m)
 #pragma unroll
       for (int S2 = 0; S2 < 2; ++S2)
 #pragma unroll
-        for (int i = 2 * S2; i < 4; ++i) qs[i] = mfma_bf16(uf[S2].p[m], pf[low_block(i >> 1, i & 1, S2)], qs[i]);
+        for (int i = 2 * S2; i < 4; ++i) qo[i] = mfma_bf16(uf[S2].p[m], pf[low_block(i >> 1, i & 1, S2)], qo[i]);
     const int start = sp.start + (c - c0) * C, len = min(C, sp.end - start);
     const uint32_t vrow = (uint32_t)a.H * a.P * 2;
     const brsrc ro = make_rsrc((char*)a.out + (((int64_t)start * a.H + h) * a.P + p0) * 2,
                                (uint32_t)(len - 1) * vrow + pw * 2);
 #pragma unroll
     for (int i = 0; i < 4; ++i)
-      store4io(ro, (32 * (i >> 1) + row32(r, i & 1)) * vrow + (16 * tile + 4 * q) * 2, qs[i], IoBf16{});
+      store4io(ro, (32 * (i >> 1) + row32(r, i & 1)) * vrow + (16 * tile + 4 * q) * 2, qo[i], IoBf16{});
   };
 
   if (c0 < c1) {
@@ -300,16 +316,23 @@ __global__ __launch_bounds__(64 * NPT + 256, 1) void delta_fwd_kernel(DeltaArgs 
     load_r(c0);
     load_p(c0);
     put_kqv(0);
-    if (c0 + 1 < c1) load_kqv(c0 + 1);
+    put_r(0);
+    if (c0 + 1 < c1) {
+      load_kqv(c0 + 1);
+      load_r(c0 + 1);
+    }
   }
+#pragma unroll
+  for (int i = 0; i < 4; ++i) qs[i] = zero;
   __syncthreads();
   for (int c = c0; c < c1; ++c) {
     // interval A
-#pragma unroll
-    for (int i = 0; i < RC; ++i) *(u32x4*)(Rl + (ht + i * 256) * 8) = xr[i];
-    if (c + 1 < c1) load_r(c + 1);
-    if (c > c0) finish(c - 1);
+    if (c > c0) {
+      put_p();  // of c - 1
+      load_p(c);
+    }
     if (outs) {
+      if (c > c0) take();
       const float* g = gl[(c - c0) & 1];
 #pragma unroll
       for (int i = 0; i < 4; ++i) qs[i] = zero;
@@ -338,17 +361,23 @@ __global__ __launch_bounds__(64 * NPT + 256, 1) void delta_fwd_kernel(DeltaArgs 
     }
     __syncthreads();
     // interval B
-#pragma unroll
-    for (int i = 0; i < 2; ++i)
-      if ((ht + i * 256) * 8 < EP) *(u32x4*)(Pl + (ht + i * 256) * 8) = xp[i];
     if (c + 1 < c1) {
-      load_p(c + 1);
       put_kqv((c + 1 - c0) & 1);
-      if (c + 2 < c1) load_kqv(c + 2);
+      put_r((c + 1 - c0) & 1);
+      if (c + 2 < c1) {
+        load_kqv(c + 2);
+        load_r(c + 2);
+      }
     }
+    if (outs && c > c0) finish(c - 1);
     __syncthreads();
   }
-  if (c0 < c1) finish(c1 - 1);
+  if (c0 < c1) {
+    put_p();
+    if (outs) take();
+  }
+  __syncthreads();
+  if (outs && c0 < c1) finish(c1 - 1);
 }
 
 hipError_t launch_delta_fwd(const DeltaProb& p, const DeltaArgs& a, hipStream_t st) {

@@ -24,6 +24,7 @@ template <int N, int P, class IO>
 __global__ __launch_bounds__(512) void delta_grads_kernel(DeltaArgs a) {
   using T = typename IO::T;
   constexpr int PI = IO::PI, PM = IO::PM, ES = sizeof(T), C = kDeltaChunk, NTH = 512;
+  constexpr int NP = N < 32 ? 32 : N;
   // columns of headdim staged at a time (the products' depth is 32; past P they are zero)
   constexpr int PB = P < 32 ? 32 : (P > (PM == 2 ? 64 : 32) ? (PM == 2 ? 64 : 32) : P), NB = (P + PB - 1) / PB;
   constexpr int LN = N + 8, LP = PB + 8, LC = C + 8;  // rows: dstate; headdim; tokens
@@ -34,7 +35,7 @@ __global__ __launch_bounds__(512) void delta_grads_kernel(DeltaArgs a) {
   uint16_t *Sl = lds, *Dl = Sl + PM * SPL, *Ul = Dl + PM * SPL, *Xl = Ul + PM * UPL, *Ol = Xl + PM * UPL;
   uint16_t *Kl = lds, *Ql = Kl + PI * KPL, *Pl = Ql + PI * KPL, *Ml = Pl + PM * CPL;
   __shared__ __align__(16) float gl[3 * C];
-  __shared__ float red[2][2][C], sd[NTH / 64], bsum[NTH / 64][C];
+  __shared__ float red[2][2][C], sd[NTH / 64], bsum[2][C];
 
   const int tid = threadIdx.x, w = __builtin_amdgcn_readfirstlane(tid >> 6), lane = tid & 63, q = lane >> 4, r = lane & 15;
   const int tb = w & 3, nh = w >> 2, tok = 16 * tb + r;
@@ -56,10 +57,10 @@ __global__ __launch_bounds__(512) void delta_grads_kernel(DeltaArgs a) {
   for (int hh = 0; hh < per; ++hh) {
     const int h = grp * per + hh;
     const int64_t kh = (int64_t)ck * a.H + h;
-    const float* S = a.S + kh * P * N;
-    const float* dS = a.dS + kh * P * N;
-    const float* Z = a.Z + kh * C * P;
-    const float* F = a.F + kh * C * P;
+    const f32x4* S = (const f32x4*)(a.S + kh * P * NP);
+    const f32x4* dS = (const f32x4*)(a.dS + kh * P * NP);
+    const f32x4* Z = (const f32x4*)(a.Z + kh * C * P);
+    const f32x4* F = (const f32x4*)(a.F + kh * C * P);
     const brsrc ro = make_rsrc((const char*)a.dout + ((int64_t)start * a.H + h) * P * ES,
                                (uint32_t)(len - 1) * vrow + P * ES);
     const brsrc rdv = make_rsrc((char*)a.dv + ((int64_t)start * a.H + h) * P * ES, (uint32_t)(len - 1) * vrow + P * ES);
@@ -70,52 +71,50 @@ __global__ __launch_bounds__(512) void delta_grads_kernel(DeltaArgs a) {
 #pragma unroll
     for (int i = 0; i < 4; ++i) cc[i] = zero;
     float sdot = 0.f;
-    f32x4 bdot[2] = {zero, zero};  // F . Z of eight tokens, this thread's rows
+    f32x4 bdot = zero;  // F . Z of four tokens, this thread's rows
+    const int tk4 = 32 * ((w & 3) >> 1) + 8 * q + 4 * (w & 1);
     __syncthreads();
 #pragma unroll 1
     for (int pb = 0; pb < NB; ++pb) {
-      // stage the states (PB x N) and the token rows (64 x PB) as planes
-      constexpr int SE = PB * N / 4;
+      // stage the states (PB x N), Z and F as U and dX (PB x 64), and dO (64 x PB) as planes; a
+      // wave reads whole tiles (delta.hpp)
+      constexpr int SE = PB * NP / 4, RE = PB * C / 4;
 #pragma unroll 4
       for (int e = tid; e < SE; e += NTH) {
-        const int row = e / (N / 4), col = (e % (N / 4)) * 4, p = pb * PB + row;
+        const int tile = e >> 6, row = tile / (NP / 16) * 16 + r, col = 32 * ((tile % (NP / 16)) >> 1) + 8 * q + 4 * (tile & 1);
         f32x4 x = zero, y = zero;
-        if (p < P) {
-          x = *(const f32x4*)(S + (int64_t)p * N + col);
-          y = *(const f32x4*)(dS + (int64_t)p * N + col);
+        if (pb * PB + row < P && (N == NP || col < N)) {
+          x = S[pb * SE + e];
+          y = dS[pb * SE + e];
         }
         sdot += x[0] * y[0] + x[1] * y[1] + x[2] * y[2] + x[3] * y[3];
-        uint2 o[PM];
-        split4<PM>(x, o);
+        if (N == NP || col < N) {
+          uint2 o[PM];
+          split4<PM>(x, o);
 #pragma unroll
-        for (int m = 0; m < PM; ++m) *(uint2*)(Sl + m * SPL + row * LN + col) = o[m];
-        split4<PM>(y, o);
+          for (int m = 0; m < PM; ++m) *(uint2*)(Sl + m * SPL + row * LN + col) = o[m];
+          split4<PM>(y, o);
 #pragma unroll
-        for (int m = 0; m < PM; ++m) *(uint2*)(Dl + m * SPL + row * LN + col) = o[m];
+          for (int m = 0; m < PM; ++m) *(uint2*)(Dl + m * SPL + row * LN + col) = o[m];
+        }
       }
-      // Z and F (PB x 64, tokens fastest) as planes of U and dX, and dO (64 x PB)
-      if (tid < PB * C / 8) {
-        const int row = tid / (C / 8), p = pb * PB + row, t8 = (tid % (C / 8)) * 8;
-        f32x4 z[2] = {zero, zero}, f[2] = {zero, zero}, b[2];
-        if (p < P) {
 #pragma unroll
-          for (int i = 0; i < 2; ++i) {
-            z[i] = *(const f32x4*)(Z + p * C + t8 + 4 * i);
-            f[i] = *(const f32x4*)(F + p * C + t8 + 4 * i);
-          }
+      for (int e = tid; e < RE; e += NTH) {  // (a thread's tokens are the same every time)
+        const int row = (e >> 8) * 16 + r;
+        f32x4 z = zero, f = zero;
+        if (pb * PB + row < P) {
+          z = Z[pb * RE + e];
+          f = F[pb * RE + e];
         }
+        bdot += z * f;
+        const f32x4 b = *(const f32x4*)(gl + 2 * C + tk4);
+        uint2 o[PM];
+        split4<PM>(b * z, o);
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-          b[i] = *(const f32x4*)(gl + 2 * C + t8 + 4 * i);
-          bdot[i] += z[i] * f[i];
-        }
-        u32x4 o[PM];
-        split8<PM>(b[0] * z[0], b[1] * z[1], o);
+        for (int m = 0; m < PM; ++m) *(uint2*)(Ul + m * UPL + row * LC + tk4) = o[m];
+        split4<PM>(b * f, o);
 #pragma unroll
-        for (int m = 0; m < PM; ++m) *(u32x4*)(Ul + m * UPL + row * LC + t8) = o[m];
-        split8<PM>(b[0] * f[0], b[1] * f[1], o);
-#pragma unroll
-        for (int m = 0; m < PM; ++m) *(u32x4*)(Xl + m * UPL + row * LC + t8) = o[m];
+        for (int m = 0; m < PM; ++m) *(uint2*)(Xl + m * UPL + row * LC + tk4) = o[m];
       }
       if (tid < C * PB / 8) {
         const int t = tid / (PB / 8), col = (tid % (PB / 8)) * 8, p = pb * PB + col;
@@ -244,17 +243,12 @@ __global__ __launch_bounds__(512) void delta_grads_kernel(DeltaArgs a) {
     }
     sdot = wave_sum(sdot);
     if (lane == 0) sd[w] = sdot;
-    // F . Z over the rows of a wave (lanes eight apart), in order over the waves below
+    // F . Z over the rows: 16 lanes, then two waves in order
 #pragma unroll
-    for (int i = 0; i < 2; ++i)
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        float v = bdot[i][e];
-        v += __shfl_xor(v, 8);
-        v += __shfl_xor(v, 16);
-        v += __shfl_xor(v, 32);
-        if (lane < 8) bsum[w][lane * 8 + 4 * i + e] = v;
-      }
+    for (int e = 0; e < 4; ++e) {
+      const float v = row_sum16(bdot[e]);
+      if (r == 0) bsum[w >> 2][tk4 + e] = v;
+    }
     __syncthreads();
     if (w == 0) {
       double x = (double)red[0][0][lane] + (double)red[0][1][lane];
@@ -274,9 +268,7 @@ __global__ __launch_bounds__(512) void delta_grads_kernel(DeltaArgs a) {
       if (lane < len) {
         const int64_t at = ((int64_t)start + lane) * a.H + h;
         a.dg[at] = (float)(x + (y - wj));
-        float v = bsum[0][lane];
-        for (int i = 1; i < NTH / 64; ++i) v += bsum[i][lane];
-        a.dbeta[at] = v;
+        a.dbeta[at] = bsum[0][lane] + bsum[1][lane];
       }
     }
     // (the next head's first barrier is behind these reads: gl is rewritten before it)
