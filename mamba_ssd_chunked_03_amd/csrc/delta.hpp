@@ -58,7 +58,7 @@ struct DeltaArgs {
   void* out;
   float* final_states;
   float* gates;                // (nck, H, kDeltaGates): see below
-  uint16_t *R, *Pm, *Rt, *Pt;  // plane-split chunk matrices in fragment order (null: not kept)
+  uint16_t *R, *Pm, *Rt, *Pt;  // plane-split chunk matrices in operand order (null: not kept)
   float *S, *Z;                // kept for the backward: states entering each chunk, Z (tile order)
   // backward
   const void* dout;
@@ -70,8 +70,9 @@ struct DeltaArgs {
 };
 
 // Per (chunk, head), 64 tokens each: running log2 decay G (high part, low part), beta; and
-// where io is bf16 exp(G), exp(G_C - G).  Past the chunk's end G stays and beta is zero.
-constexpr int kDeltaGates = 5 * kDeltaChunk;
+// where io is bf16 exp(G), beta exp(G_C - G), exp(G_C - G), beta exp(G).  Past the chunk's
+// end G stays and beta is zero.
+constexpr int kDeltaGates = 7 * kDeltaChunk;
 
 // States and their adjoints per (chunk, head), and Z and F, are kept in the order of the
 // chains' accumulator tiles, 16 columns of headdim after the other, so that a wave stores

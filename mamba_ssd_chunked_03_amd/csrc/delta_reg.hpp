@@ -59,6 +59,16 @@ __device__ __forceinline__ Planes<NP> tile_planes(f32x4 a, f32x4 b) {
   return f;
 }
 
+// Scheduling pattern of the region before it: M matrix instructions, V vector ones after each.
+template <int M, int V>
+__device__ __forceinline__ void interleave() {
+#pragma unroll
+  for (int i = 0; i < M; ++i) {
+    __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+    __builtin_amdgcn_sched_group_barrier(0x002, V, 0);
+  }
+}
+
 // (sequence, workgroup of the sequence) of a chain's workgroup: each XCD takes the same part
 // of every sequence's `per` workgroups (heads of one group share K and Q in its L2), so that
 // a long sequence among short ones is spread over all of them.

@@ -3,13 +3,13 @@
 // chunk, from what the forward kept (R and P transposed, the gates).  With U = b Z and
 // O = scale exp(G) Q S^T + P U, per chunk:
 //   E = P^T dO + exp(G_C - G) K dS^T          (adjoint of U)
-//   F = E - R^T (b E),   dX = b F = dV         (adjoints of U in full, and of X)
+//   F = E - (b R)^T E,   dX = b F = dV         (adjoints of U in full, and of X)
 //   dS <- exp(G_C) dS + (scale exp(G) dO)^T Q - (exp(G) dX)^T K
 // F and the dS of every chunk are stored for k_delta_grads.hip, which forms the gradients
 // chunk by chunk.  Registers, waves and tiles as in k_delta_fwd.hip.  The helper waves form
 // what does not wait for dS a chunk ahead: E0 = P^T dO and T = (scale exp(G) dO)^T Q.
 //   interval A(c)  chain: K dS^T, E                 helpers: T(c), Q, P, dO(c - 1) to LDS
-//   interval B(c)  chain: R^T (b E), F, the new dS   helpers: K, R(c - 1) to LDS, E0, T of c - 1
+//   interval B(c)  chain: (b R)^T E, F, the new dS   helpers: K, R(c - 1) to LDS, E0, T of c - 1
 // Two planes throughout (the error of dS is not a result: 3e-6 of the gradients).
 #include "delta_reg.hpp"
 
@@ -21,7 +21,7 @@ __global__ __launch_bounds__(64 * NPT + 256, 1) void delta_bwd_kernel(DeltaArgs 
   using Tile = TokTile<NP>;
   constexpr int LV = 16 * NPT + 8, EV = C * LV, ER = 2 * kTriPlane;
   __shared__ __align__(16) uint16_t Kl[2][Tile::SIZE], Ql[Tile::SIZE], Rl[2][ER], Pl[ER], Ol[EV];
-  __shared__ __align__(16) float gl[2][3 * C];  // beta, exp(G), exp(G_C - G)
+  __shared__ __align__(16) float gl[2][3 * C];  // exp(G), exp(G_C - G), beta exp(G)
   __shared__ __align__(16) f32x4 Ex[NPT][4][64], Tx[NPT][KS][2][64];  // E0 and T, tile order
 
   const int tid = threadIdx.x, w = __builtin_amdgcn_readfirstlane(tid >> 6), lane = tid & 63, q = lane >> 4, r = lane & 15;
@@ -48,9 +48,6 @@ __global__ __launch_bounds__(64 * NPT + 256, 1) void delta_bwd_kernel(DeltaArgs 
 #pragma unroll
       for (int t = 0; t < 2; ++t)
         S[k][t] = a.d_final && live && scol(k, t) < N ? *(const f32x4*)(a.d_final + srow + scol(k, t)) : zero;
-    Planes<2> sf[KS];
-#pragma unroll
-    for (int k = 0; k < KS; ++k) sf[k] = tile_planes<2>(S[k][0], S[k][1]);
     f32x4* kS = (f32x4*)a.dS + (int64_t)(pc >> 4) * (KS * 2) * 64 + lane;  // of chunk slot 0
     f32x4* kF = (f32x4*)a.F + (int64_t)(pc >> 4) * 4 * 64 + lane;
     __syncthreads();
@@ -59,112 +56,122 @@ __global__ __launch_bounds__(64 * NPT + 256, 1) void delta_bwd_kernel(DeltaArgs 
       const uint16_t* K = Kl[(c1 - 1 - c) & 1];
       const float* g = gl[(c1 - 1 - c) & 1];
       const int64_t kh = (int64_t)c * a.H + h;
-      // interval A: E, tile i = 2B + t with tokens 32B + 8q + 4t + e
-      f32x4 E[4], bt[4], eg[4];
-      bf16x8 kt[KS][2];
-      Planes<2> Rf[6];
-      const float eC = g[C + C - 1];
-      {
-        bf16x8 kf[2][4];
-        f32x4 ks[4];
-        auto fetch = [&](int k) {
+      // interval A: E, tile i = 2B + t with tokens 32B + 8q + 4t + e; block 1 of the tokens with
+      // dS's planes on the way, block 0 with E of block 1
+      f32x4 ks[4], E[4], er[4], wg4[4];
+      Planes<2> ef[2], Rf[6];
+      bf16x8 kt[KS][2][2];  // K^T, by block of tokens
+      const float eC = g[C - 1];
+      bf16x8 kf[KS][2], kg[KS][2];
+      Planes<2> sf[KS];
 #pragma unroll
-          for (int i = 0; i < 4; ++i) kf[k & 1][i] = tok_rows<NP>(K, 32 * (i >> 1), i & 1, 32 * k, lane);
-        };
-        fetch(0);
+      for (int k = 0; k < KS; ++k)
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          ks[i] = zero;
-          E[i] = Ex[w][i][lane];
-          bt[i] = *(const f32x4*)(g + 32 * (i >> 1) + 8 * q + 4 * (i & 1));
-        }
-        __builtin_amdgcn_sched_barrier(0);
+        for (int t = 0; t < 2; ++t) kf[k][t] = tok_rows<NP>(K, 32, t, 32 * k, lane);
 #pragma unroll
-        for (int k = 0; k < KS; ++k) {
-          if (k + 1 < KS) fetch(k + 1);
-          __builtin_amdgcn_sched_barrier(0);
-#pragma unroll
-          for (int m = 1; m >= 0; --m)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) ks[i] = mfma_bf16(kf[k & 1][i], sf[k].p[m], ks[i]);
-          if (live)
-#pragma unroll
-            for (int t = 0; t < 2; ++t) kS[(kh * (a.P / 16) * (KS * 2) + k * 2 + t) * 64] = S[k][t];
-          __builtin_amdgcn_sched_barrier(0);
-        }
-        // what the next interval starts with, under way while E is formed
-#pragma unroll
-        for (int i = 0; i < 6; ++i)
-#pragma unroll
-          for (int m = 0; m < 2; ++m)
-            Rf[i].p[m] = as_bf16x8(*(const u32x4*)(Rl[(c1 - 1 - c) & 1] + m * kTriPlane + i * 512 + lane * 8));
-#pragma unroll
-        for (int i = 0; i < 4; ++i) eg[i] = *(const f32x4*)(g + C + 32 * (i >> 1) + 8 * q + 4 * (i & 1));
-#pragma unroll
-        for (int k = 0; k < KS; ++k)
-#pragma unroll
-          for (int t = 0; t < 2; ++t) kt[k][t] = tok_cols<NP>(K, 0, t, 32 * k, lane);
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-          E[i] += *(const f32x4*)(g + 2 * C + 32 * (i >> 1) + 8 * q + 4 * (i & 1)) * ks[i];
+      for (int i = 0; i < 4; ++i) {
+        ks[i] = zero;
+        E[i] = Ex[w][i][lane];
+        er[i] = *(const f32x4*)(g + C + 32 * (i >> 1) + 8 * q + 4 * (i & 1));
+        wg4[i] = *(const f32x4*)(g + 2 * C + 32 * (i >> 1) + 8 * q + 4 * (i & 1));
       }
-      Planes<2> ef[2];
 #pragma unroll
-      for (int B = 0; B < 2; ++B) ef[B] = tile_planes<2>(bt[2 * B] * E[2 * B], bt[2 * B + 1] * E[2 * B + 1]);
+      for (int k = 0; k < KS; ++k)
+#pragma unroll
+        for (int t = 0; t < 2; ++t) kg[k][t] = tok_rows<NP>(K, 0, t, 32 * k, lane);
+      sf[0] = tile_planes<2>(S[0][0], S[0][1]);
+      __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+      for (int k = 0; k < KS; ++k) {
+#pragma unroll
+        for (int m = 1; m >= 0; --m)
+#pragma unroll
+          for (int t = 0; t < 2; ++t) ks[2 + t] = mfma_bf16(kf[k][t], sf[k].p[m], ks[2 + t]);
+        if (k + 1 < KS) sf[k + 1] = tile_planes<2>(S[k + 1][0], S[k + 1][1]);
+        if (live)
+#pragma unroll
+          for (int t = 0; t < 2; ++t) kS[(kh * (a.P / 16) * (KS * 2) + k * 2 + t) * 64] = S[k][t];
+        interleave<4, 4>();
+        __builtin_amdgcn_sched_barrier(0);
+      }
+      auto form_e = [&](int B) {
+#pragma unroll
+        for (int i = 2 * B; i < 2 * B + 2; ++i) E[i] += er[i] * ks[i];
+        ef[B] = tile_planes<2>(E[2 * B], E[2 * B + 1]);
+      };
+      // (and what the next interval starts with)
+#pragma unroll
+      for (int i = 0; i < 6; ++i)
+#pragma unroll
+        for (int m = 0; m < 2; ++m)
+          Rf[i].p[m] = as_bf16x8(*(const u32x4*)(Rl[(c1 - 1 - c) & 1] + m * kTriPlane + i * 512 + lane * 8));
+#pragma unroll
+      for (int k = 0; k < KS; ++k)
+#pragma unroll
+        for (int t = 0; t < 2; ++t) kt[k][t][1] = tok_cols<NP>(K, 32, t, 32 * k, lane);
+      __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+      for (int k = 0; k < KS; ++k)
+#pragma unroll
+        for (int m = 1; m >= 0; --m)
+#pragma unroll
+          for (int t = 0; t < 2; ++t) ks[t] = mfma_bf16(kg[k][t], sf[k].p[m], ks[t]);
+      form_e(1);
+      interleave<4 * KS, 3>();
+      __builtin_amdgcn_sched_barrier(0);
+      form_e(0);
       __syncthreads();
-      // interval B: F = E - R^T (b E), by planes
+      // interval B: F = E - (b R)^T E, by planes, with dS's decay on the way
       f32x4 F[4];
 #pragma unroll
       for (int i = 0; i < 4; ++i) F[i] = zero;
 #pragma unroll
+      for (int k = 0; k < KS; ++k)
+#pragma unroll
+        for (int t = 0; t < 2; ++t) kt[k][t][0] = tok_cols<NP>(K, 0, t, 32 * k, lane);
+      __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
       for (int m = 0; m < 3; ++m)
 #pragma unroll
-        for (int B2 = 1; B2 >= 0; --B2)
+        for (int t = 0; t < 2; ++t) F[2 + t] = mfma_bf16(Rf[up_block(1, t, 1)].p[m == 0], ef[1].p[m == 1], F[2 + t]);
 #pragma unroll
-          for (int i = 0; i < (B2 ? 4 : 2); ++i)
-            F[i] = mfma_bf16(Rf[up_block(i >> 1, i & 1, B2)].p[m == 0], ef[B2].p[m == 1], F[i]);
+      for (int B2 = 1; B2 >= 0; --B2)
+#pragma unroll
+        for (int m = 0; m < 3; ++m)
+#pragma unroll
+          for (int t = 0; t < 2; ++t) F[t] = mfma_bf16(Rf[up_block(0, t, B2)].p[m == 0], ef[B2].p[m == 1], F[t]);
 #pragma unroll
       for (int k = 0; k < KS; ++k)
 #pragma unroll
         for (int t = 0; t < 2; ++t) S[k][t] = eC * S[k][t] + Tx[w][k][t][lane];
+      interleave<18, 2>();
+      __builtin_amdgcn_sched_barrier(0);
       Planes<2> wf[2];
-#pragma unroll
-      for (int B = 0; B < 2; ++B) {
+      auto form_w = [&](int B) {
         f32x4 wv[2];
 #pragma unroll
         for (int t = 0; t < 2; ++t) {
           const int i = 2 * B + t;
           F[i] = E[i] - F[i];
           if (live) kF[(kh * (a.P / 16) * 4 + i) * 64] = F[i];
-          wv[t] = -eg[i] * (bt[i] * F[i]);
+          wv[t] = -(wg4[i] * F[i]);
         }
         wf[B] = tile_planes<2>(wv[0], wv[1]);
-      }
+      };
+      form_w(1);
+      __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-      for (int B = 0; B < 2; ++B) {
-        bf16x8 kn[KS][2];
-        if (B == 0) {
-#pragma unroll
-          for (int k = 0; k < KS; ++k)
-#pragma unroll
-            for (int t = 0; t < 2; ++t) kn[k][t] = tok_cols<NP>(K, 32, t, 32 * k, lane);
-        }
-        __builtin_amdgcn_sched_barrier(0);
+      for (int B = 1; B >= 0; --B) {
 #pragma unroll
         for (int m = 1; m >= 0; --m)
 #pragma unroll
           for (int k = 0; k < KS; ++k)
 #pragma unroll
-            for (int t = 0; t < 2; ++t) S[k][t] = mfma_bf16(kt[k][t], wf[B].p[m], S[k][t]);
-        if (B == 0) {
-#pragma unroll
-          for (int k = 0; k < KS; ++k)
-#pragma unroll
-            for (int t = 0; t < 2; ++t) kt[k][t] = kn[k][t];
-        }
+            for (int t = 0; t < 2; ++t) S[k][t] = mfma_bf16(kt[k][t][B], wf[B].p[m], S[k][t]);
+        if (B == 1) form_w(0);
+        interleave<4 * KS, 2>();
+        __builtin_amdgcn_sched_barrier(0);
       }
-#pragma unroll
-      for (int k = 0; k < KS; ++k) sf[k] = tile_planes<2>(S[k][0], S[k][1]);
       __syncthreads();
     }
     if (a.d_init && live) {
@@ -232,7 +239,8 @@ __global__ __launch_bounds__(64 * NPT + 256, 1) void delta_bwd_kernel(DeltaArgs 
     const brsrc rp = make_rsrc(a.Pt + kh * ER, ER * 2);
 #pragma unroll
     for (int i = 0; i < RC; ++i) xp[i] = buf_load16(rp, (ht + i * 256) * 16);
-    xg = buf_load_f32(make_rsrc(a.gates + kh * kDeltaGates + 2 * C, 3 * C * 4), ht * 4);
+    const int gi = ht < C ? 3 * C + ht : 4 * C + ht;  // exp(G); exp(G_C - G), beta exp(G)
+    xg = buf_load_f32(make_rsrc(a.gates + kh * kDeltaGates, kDeltaGates * 4), gi * 4);
   };
   auto put_k = [&](int buf) {
 #pragma unroll
@@ -290,7 +298,7 @@ __global__ __launch_bounds__(64 * NPT + 256, 1) void delta_bwd_kernel(DeltaArgs 
       f32x4 d[2];
 #pragma unroll
       for (int t = 0; t < 2; ++t)
-        d[t] = (a.scale * *(const f32x4*)(g + C + 32 * B + 8 * q + 4 * t)) *
+        d[t] = (a.scale * *(const f32x4*)(g + 32 * B + 8 * q + 4 * t)) *
                f32x4{bf_lo(ow[2 * t]), bf_hi(ow[2 * t]), bf_lo(ow[2 * t + 1]), bf_hi(ow[2 * t + 1])};
       df[B] = tile_planes<2>(d[0], d[1]);
     }
@@ -314,6 +322,8 @@ __global__ __launch_bounds__(64 * NPT + 256, 1) void delta_bwd_kernel(DeltaArgs 
           for (int t = 0; t < 2; ++t) T[k][t] = mfma_bf16(qf[k][t], df[B].p[m], T[k][t]);
     }
   };
+  // (The loads run on to the first chunk again instead of stopping under a branch, at whose
+  // join they would be waited for.)
   if (c0 < c1) {
     load_ahead(c1 - 1);
     load_k(c1 - 1);
@@ -321,11 +331,9 @@ __global__ __launch_bounds__(64 * NPT + 256, 1) void delta_bwd_kernel(DeltaArgs 
     put_ahead(0);
     put_k(0);
     put_r(0);
-    if (c1 - 2 >= c0) {
-      load_ahead(c1 - 2);
-      load_k(c1 - 2);
-      load_r(c1 - 2);
-    }
+    load_ahead(max(c1 - 2, c0));
+    load_k(max(c1 - 2, c0));
+    load_r(max(c1 - 2, c0));
   }
   __syncthreads();
   if (c0 < c1) ahead(0);
@@ -339,21 +347,15 @@ __global__ __launch_bounds__(64 * NPT + 256, 1) void delta_bwd_kernel(DeltaArgs 
 #pragma unroll
         for (int t = 0; t < 2; ++t) Tx[tile][k][t][lane] = T[k][t];
     }
-    if (c > c0) {
-      put_ahead(nb);
-      if (c - 2 >= c0) load_ahead(c - 2);
-    }
+    put_ahead(nb);
+    load_ahead(max(c - 2, c0));
     __syncthreads();
     // interval B
-    if (c > c0) {
-      put_k(nb);
-      put_r(nb);
-      if (c - 2 >= c0) {
-        load_k(c - 2);
-        load_r(c - 2);
-      }
-      ahead(nb);
-    }
+    put_k(nb);
+    put_r(nb);
+    load_k(max(c - 2, c0));
+    load_r(max(c - 2, c0));
+    ahead(nb);
     __syncthreads();
   }
 }

@@ -8,11 +8,14 @@
 //   product's accumulator tiles are the next product's operand (delta_reg.hpp); K, R, V
 //   come through LDS.
 // * The helpers keep memory away from the chain: they load the chunks ahead into
-//   registers and copy them to LDS, and the first NPT of them form the output, one
-//   chunk's P U behind the chain, from the planes of S and U that the chain leaves in LDS.
+//   registers and copy them to LDS, and the first NPT of them form the output half a chunk
+//   behind the chain, from the planes of S and from Z, which it leaves in LDS.
 // Two barriers a chunk:
-//   interval A(c)  chain: K S^T, X                  helpers: P(c - 1) to LDS, Q S^T of c
-//   interval B(c)  chain: R (b X), U, the new S     helpers: K, Q, R, V(c + 1) to LDS, O of c - 1
+//   interval A(c)  chain: S's planes, K S^T, X    helpers: Q(c) to LDS, O of c - 1
+//   interval B(c)  chain: (R b) X, Z, the new S    helpers: K, R, V(c + 1), P(c) to LDS, Q S^T of c
+// A matrix instruction occupies the matrix core for 16 cycles and the issue of its wave for
+// four: the chain's vector work (planes, scalings: 240 instructions a chunk) is placed
+// between the products that do not wait for it, two a product.
 // A compute unit takes in 50 KB a chunk whatever NPT is (58 KB with V and O at NPT = 4),
 // 1000 cycles of its load path at the least and 2000 when they come from HBM: issued by the
 // waves that compute, those loads held up everything behind them.
@@ -30,8 +33,9 @@ __global__ __launch_bounds__(64 * NPT + 256, 1) void delta_fwd_kernel(DeltaArgs 
   using Tile = TokTile<NP>;
   constexpr int LV = 16 * NPT + 8, EV = C * LV, ER = 2 * kTriPlane, EP = kTriPlane;
   __shared__ __align__(16) uint16_t Kl[2][Tile::SIZE], Ql[Tile::SIZE], Rl[2][ER], Pl[EP], Vl[EV];
-  __shared__ __align__(16) float gl[2][3 * C];  // beta, exp(G), exp(G_C - G)
-  __shared__ __align__(16) u32x4 Sx[NPT][KS][2][64], Ux[NPT][2][2][64];  // planes of S and U, operand order
+  __shared__ __align__(16) float gl[2][3 * C];  // beta, exp(G), beta exp(G_C - G)
+  __shared__ __align__(16) u32x4 Sx[NPT][KS][2][64];  // planes of S, operand order
+  __shared__ __align__(16) f32x4 Zx[NPT][4][64];      // Z, tile order
 
   const int tid = threadIdx.x, w = __builtin_amdgcn_readfirstlane(tid >> 6), lane = tid & 63, q = lane >> 4, r = lane & 15;
   const int np = (ptiles + NPT - 1) / NPT;
@@ -58,139 +62,139 @@ __global__ __launch_bounds__(64 * NPT + 256, 1) void delta_fwd_kernel(DeltaArgs 
 #pragma unroll
       for (int t = 0; t < 2; ++t)
         S[k][t] = a.init && live && scol(k, t) < N ? *(const f32x4*)(a.init + srow + scol(k, t)) : zero;
-    Planes<2> sf[KS];
-    auto put_state = [&]() {
-#pragma unroll
-      for (int k = 0; k < KS; ++k) {
-        sf[k] = tile_planes<2>(S[k][0], S[k][1]);
-#pragma unroll
-        for (int m = 0; m < 2; ++m) Sx[w][k][m][lane] = __builtin_bit_cast(u32x4, sf[k].p[m]);
-      }
-    };
     f32x4* kS = (f32x4*)a.S + (int64_t)(pc >> 4) * (KS * 2) * 64 + lane;  // of chunk slot 0 (SAVE)
     f32x4* kZ = (f32x4*)a.Z + (int64_t)(pc >> 4) * 4 * 64 + lane;
-    put_state();
     __syncthreads();
     for (int c = c0; c < c1; ++c) {
       const uint16_t* K = Kl[(c - c0) & 1];
       const float* g = gl[(c - c0) & 1];
       const int64_t kh = (int64_t)c * a.H + h;
-      // interval A: K S^T, tile i = 2B + t with tokens 32B + 8q + 4t + e
-      f32x4 ks[4], bt[4];
+      // interval A: K S^T, tile i = 2B + t with tokens 32B + 8q + 4t + e; block 0 of the tokens
+      // with S's planes on the way, block 1 with X of block 0
+      f32x4 ks[4], X[4], eg[4], wg4[4];
       u32x4 vw[2];
-      {
-        bf16x8 kf[2][4];
-        auto fetch = [&](int k) {
+      Planes<2> xf[2], Rf[6];
+      bf16x8 kt[KS][2][2];  // K^T, by block of tokens
+      const float eC = g[C + C - 1];
+      bf16x8 kf[KS][2], kg[KS][2];
+      Planes<2> sf[KS];
 #pragma unroll
-          for (int i = 0; i < 4; ++i) kf[k & 1][i] = tok_rows<NP>(K, 32 * (i >> 1), i & 1, 32 * k, lane);
-        };
-        fetch(0);
+      for (int k = 0; k < KS; ++k)
 #pragma unroll
-        for (int B = 0; B < 2; ++B) vw[B] = __builtin_bit_cast(u32x4, frag_kmajor(Vl + 32 * B * LV + 16 * w, LV, lane));
+        for (int t = 0; t < 2; ++t) kf[k][t] = tok_rows<NP>(K, 0, t, 32 * k, lane);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          ks[i] = zero;
-          bt[i] = *(const f32x4*)(g + 32 * (i >> 1) + 8 * q + 4 * (i & 1));
-        }
-        __builtin_amdgcn_sched_barrier(0);
+      for (int B = 0; B < 2; ++B) vw[B] = __builtin_bit_cast(u32x4, frag_kmajor(Vl + 32 * B * LV + 16 * w, LV, lane));
 #pragma unroll
-        for (int k = 0; k < KS; ++k) {
-          if (k + 1 < KS) fetch(k + 1);
-          __builtin_amdgcn_sched_barrier(0);
-#pragma unroll
-          for (int m = 1; m >= 0; --m)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) ks[i] = mfma_bf16(kf[k & 1][i], sf[k].p[m], ks[i]);
-          if constexpr (SAVE)
-            if (live)
-#pragma unroll
-              for (int t = 0; t < 2; ++t) kS[(kh * (a.P / 16) * (KS * 2) + k * 2 + t) * 64] = S[k][t];
-          __builtin_amdgcn_sched_barrier(0);
-        }
+      for (int i = 0; i < 4; ++i) {
+        ks[i] = zero;
+        eg[i] = *(const f32x4*)(g + C + 32 * (i >> 1) + 8 * q + 4 * (i & 1));
+        wg4[i] = *(const f32x4*)(g + 2 * C + 32 * (i >> 1) + 8 * q + 4 * (i & 1));
       }
-      // what the next interval starts with, under way while X is formed
-      f32x4 er[4];
-      bf16x8 kt[KS][2];
-      Planes<2> Rf[6];
+#pragma unroll
+      for (int k = 0; k < KS; ++k)
+#pragma unroll
+        for (int t = 0; t < 2; ++t) kg[k][t] = tok_rows<NP>(K, 32, t, 32 * k, lane);
+      sf[0] = tile_planes<2>(S[0][0], S[0][1]);
+      __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+      for (int k = 0; k < KS; ++k) {
+#pragma unroll
+        for (int m = 1; m >= 0; --m)
+#pragma unroll
+          for (int t = 0; t < 2; ++t) ks[t] = mfma_bf16(kf[k][t], sf[k].p[m], ks[t]);
+        if (k + 1 < KS) sf[k + 1] = tile_planes<2>(S[k + 1][0], S[k + 1][1]);
+#pragma unroll
+        for (int m = 0; m < 2; ++m) Sx[w][k][m][lane] = __builtin_bit_cast(u32x4, sf[k].p[m]);
+        if constexpr (SAVE)
+          if (live)
+#pragma unroll
+            for (int t = 0; t < 2; ++t) kS[(kh * (a.P / 16) * (KS * 2) + k * 2 + t) * 64] = S[k][t];
+        interleave<4, 4>();
+        __builtin_amdgcn_sched_barrier(0);
+      }
+      auto form_x = [&](int B) {
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+          const f32x4 v = {bf_lo(vw[B][2 * t]), bf_hi(vw[B][2 * t]), bf_lo(vw[B][2 * t + 1]), bf_hi(vw[B][2 * t + 1])};
+          X[2 * B + t] = v - eg[2 * B + t] * ks[2 * B + t];
+        }
+        xf[B] = tile_planes<2>(X[2 * B], X[2 * B + 1]);
+      };
+      // (and what the next interval starts with)
 #pragma unroll
       for (int i = 0; i < 6; ++i)
 #pragma unroll
         for (int m = 0; m < 2; ++m)
           Rf[i].p[m] = as_bf16x8(*(const u32x4*)(Rl[(c - c0) & 1] + m * kTriPlane + i * 512 + lane * 8));
 #pragma unroll
-      for (int i = 0; i < 4; ++i) er[i] = *(const f32x4*)(g + 2 * C + 32 * (i >> 1) + 8 * q + 4 * (i & 1));
-      const float eC = g[C + C - 1];
+      for (int k = 0; k < KS; ++k)
+#pragma unroll
+        for (int t = 0; t < 2; ++t) kt[k][t][0] = tok_cols<NP>(K, 0, t, 32 * k, lane);
+      __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
       for (int k = 0; k < KS; ++k)
 #pragma unroll
-        for (int t = 0; t < 2; ++t) kt[k][t] = tok_cols<NP>(K, 0, t, 32 * k, lane);
-      f32x4 X[4];
-      Planes<2> xf[2];
+        for (int m = 1; m >= 0; --m)
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int B = i >> 1, t = i & 1;
-        const f32x4 v = {bf_lo(vw[B][2 * t]), bf_hi(vw[B][2 * t]), bf_lo(vw[B][2 * t + 1]), bf_hi(vw[B][2 * t + 1])};
-        X[i] = v - *(const f32x4*)(g + C + 32 * B + 8 * q + 4 * t) * ks[i];
-      }
-#pragma unroll
-      for (int B = 0; B < 2; ++B) xf[B] = tile_planes<2>(bt[2 * B] * X[2 * B], bt[2 * B + 1] * X[2 * B + 1]);
+          for (int t = 0; t < 2; ++t) ks[2 + t] = mfma_bf16(kg[k][t], sf[k].p[m], ks[2 + t]);
+      form_x(0);
+      interleave<4 * KS, 3>();
+      __builtin_amdgcn_sched_barrier(0);
+      form_x(1);
       __syncthreads();
-      // interval B: Z = X - R (b X), by planes (low x high, high x low, high x high)
+      // interval B: Z = X - (R b) X, by planes (low x high, high x low, high x high), with the
+      // state's decay on the way
       f32x4 Z[4];
 #pragma unroll
       for (int i = 0; i < 4; ++i) Z[i] = zero;
 #pragma unroll
+      for (int k = 0; k < KS; ++k)
+#pragma unroll
+        for (int t = 0; t < 2; ++t) kt[k][t][1] = tok_cols<NP>(K, 32, t, 32 * k, lane);
+      __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
       for (int m = 0; m < 3; ++m)
 #pragma unroll
-        for (int S2 = 0; S2 < 2; ++S2)
+        for (int t = 0; t < 2; ++t) Z[t] = mfma_bf16(Rf[low_block(0, t, 0)].p[m == 0], xf[0].p[m == 1], Z[t]);
 #pragma unroll
-          for (int i = 2 * S2; i < 4; ++i)
-            Z[i] = mfma_bf16(Rf[low_block(i >> 1, i & 1, S2)].p[m == 0], xf[S2].p[m == 1], Z[i]);
+      for (int S2 = 0; S2 < 2; ++S2)
+#pragma unroll
+        for (int m = 0; m < 3; ++m)
+#pragma unroll
+          for (int t = 0; t < 2; ++t) Z[2 + t] = mfma_bf16(Rf[low_block(1, t, S2)].p[m == 0], xf[S2].p[m == 1], Z[2 + t]);
 #pragma unroll
       for (int k = 0; k < KS; ++k)
 #pragma unroll
         for (int t = 0; t < 2; ++t) S[k][t] = eC * S[k][t];
+      interleave<18, 2>();
+      __builtin_amdgcn_sched_barrier(0);
       Planes<3> wf[2];
-#pragma unroll
-      for (int B = 0; B < 2; ++B) {
+      auto form_w = [&](int B) {
 #pragma unroll
         for (int t = 0; t < 2; ++t) {
           const int i = 2 * B + t;
           Z[i] = X[i] - Z[i];
+          Zx[w][i][lane] = Z[i];
           if constexpr (SAVE)
             if (live) kZ[(kh * (a.P / 16) * 4 + i) * 64] = Z[i];
-          Z[i] = bt[i] * Z[i];
         }
-        wf[B] = tile_planes<3>(er[2 * B] * Z[2 * B], er[2 * B + 1] * Z[2 * B + 1]);
-        const Planes<2> uf = tile_planes<2>(Z[2 * B], Z[2 * B + 1]);
-#pragma unroll
-        for (int m = 0; m < 2; ++m) Ux[w][B][m][lane] = __builtin_bit_cast(u32x4, uf.p[m]);
-      }
-      // the state
+        wf[B] = tile_planes<3>(wg4[2 * B] * Z[2 * B], wg4[2 * B + 1] * Z[2 * B + 1]);
+      };
+      form_w(0);
+      __builtin_amdgcn_sched_barrier(0);
+      // the state; U of the second block of tokens during the first one's products
 #pragma unroll
       for (int B = 0; B < 2; ++B) {
-        bf16x8 kn[KS][2];
-        if (B == 0) {
-#pragma unroll
-          for (int k = 0; k < KS; ++k)
-#pragma unroll
-            for (int t = 0; t < 2; ++t) kn[k][t] = tok_cols<NP>(K, 32, t, 32 * k, lane);
-        }
-        __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
         for (int m = 2; m >= 0; --m)
 #pragma unroll
           for (int k = 0; k < KS; ++k)
 #pragma unroll
-            for (int t = 0; t < 2; ++t) S[k][t] = mfma_bf16(kt[k][t], wf[B].p[m], S[k][t]);
-        if (B == 0) {
-#pragma unroll
-          for (int k = 0; k < KS; ++k)
-#pragma unroll
-            for (int t = 0; t < 2; ++t) kt[k][t] = kn[k][t];
-        }
+            for (int t = 0; t < 2; ++t) S[k][t] = mfma_bf16(kt[k][t][B], wf[B].p[m], S[k][t]);
+        if (B == 0) form_w(1);
+        interleave<6 * KS, 2>();
+        __builtin_amdgcn_sched_barrier(0);
       }
-      put_state();
       __syncthreads();
     }
     __syncthreads();
@@ -215,23 +219,34 @@ __global__ __launch_bounds__(64 * NPT + 256, 1) void delta_fwd_kernel(DeltaArgs 
         *(uint2*)(Ql + Tile::at(e, c)) = make_uint2(0u, 0u);
       }
   }
-  // 16-byte pieces of a chunk a thread: K and Q, R, P, V
+  // 16-byte pieces of a chunk a thread: K, Q, R, P, V
   constexpr int KC = (C * N / 8 + 255) / 256, RC = ER / 8 / 256, VP = 2 * NPT, VC = (C * VP + 255) / 256;
   constexpr bool KX = C * N / 8 % 256 == 0, VX = C * VP % 256 == 0;  // every thread has a piece
   u32x4 xk[KC], xq[KC], xr[RC], xp[2], xv[VC];
   float xg;
-  auto load_kqv = [&](int c) {
+  auto krsrc = [&](const void* p, int c, uint32_t& row) {
     const int start = sp.start + (c - c0) * C, len = min(C, sp.end - start);
-    const uint32_t row = (uint32_t)a.G * N * 2, span = (uint32_t)(len - 1) * row + N * 2;
-    const int64_t base = ((int64_t)start * a.G + grp) * N * 2;
-    const brsrc rk = make_rsrc((const char*)a.k + base, span), rq = make_rsrc((const char*)a.q + base, span);
+    row = (uint32_t)a.G * N * 2;
+    return make_rsrc((const char*)p + ((int64_t)start * a.G + grp) * N * 2, (uint32_t)(len - 1) * row + N * 2);
+  };
+  auto load_q = [&](int c) {
+    uint32_t row;
+    const brsrc rq = krsrc(a.q, c, row);
 #pragma unroll
     for (int i = 0; i < KC; ++i) {
       const int e = ht + i * 256;
-      const uint32_t off = KX || e < C * N / 8 ? (e / (N / 8)) * row + (e % (N / 8)) * 16 : kNoOffset;
-      xk[i] = buf_load16(rk, off);
-      xq[i] = buf_load16(rq, off);
+      xq[i] = buf_load16(rq, KX || e < C * N / 8 ? (e / (N / 8)) * row + (e % (N / 8)) * 16 : kNoOffset);
     }
+  };
+  auto load = [&](int c) {
+    uint32_t row;
+    const brsrc rk = krsrc(a.k, c, row);
+#pragma unroll
+    for (int i = 0; i < KC; ++i) {
+      const int e = ht + i * 256;
+      xk[i] = buf_load16(rk, KX || e < C * N / 8 ? (e / (N / 8)) * row + (e % (N / 8)) * 16 : kNoOffset);
+    }
+    const int start = sp.start + (c - c0) * C, len = min(C, sp.end - start);
     const uint32_t vrow = (uint32_t)a.H * a.P * 2;
     const brsrc rv = make_rsrc((const char*)a.v + (((int64_t)start * a.H + h) * a.P + p0) * 2,
                                (uint32_t)(len - 1) * vrow + pw * 2);
@@ -240,39 +255,38 @@ __global__ __launch_bounds__(64 * NPT + 256, 1) void delta_fwd_kernel(DeltaArgs 
       const int e = ht + i * 256;
       xv[i] = buf_load16(rv, (VX || e < C * VP) && 8 * (e % VP) < pw ? (e / VP) * vrow + (e % VP) * 16 : kNoOffset);
     }
-    // (through a resource: a load under a branch would be waited for at the join)
-    xg = buf_load_f32(make_rsrc(a.gates + ((int64_t)c * a.H + h) * kDeltaGates + 2 * C, 3 * C * 4), ht * 4);
-  };
-  auto load_r = [&](int c) {
-    const brsrc rr = make_rsrc(a.R + ((int64_t)c * a.H + h) * ER, ER * 2);
+    const int64_t kh = (int64_t)c * a.H + h;
+    const brsrc rr = make_rsrc(a.R + kh * ER, ER * 2);
 #pragma unroll
     for (int i = 0; i < RC; ++i) xr[i] = buf_load16(rr, (ht + i * 256) * 16);
+    xg = buf_load_f32(make_rsrc(a.gates + kh * kDeltaGates + 2 * C, 3 * C * 4), ht * 4);
   };
   auto load_p = [&](int c) {
     const brsrc rp = make_rsrc(a.Pm + ((int64_t)c * a.H + h) * EP, EP * 2);
 #pragma unroll
     for (int i = 0; i < 2; ++i) xp[i] = buf_load16(rp, (ht + i * 256) * 16);  // (the last half is past the end)
   };
-  auto put_kqv = [&](int buf) {
+  auto put_q = [&]() {
 #pragma unroll
     for (int i = 0; i < KC; ++i) {
-      const int e = ht + i * 256, o = Tile::at(e / (N / 8), (e % (N / 8)) * 8);
-      if (KX || e < C * N / 8) {
-        *(u32x4*)(Kl[buf] + o) = xk[i];
-        *(u32x4*)(Ql + o) = xq[i];
-      }
+      const int e = ht + i * 256;
+      if (KX || e < C * N / 8) *(u32x4*)(Ql + Tile::at(e / (N / 8), (e % (N / 8)) * 8)) = xq[i];
+    }
+  };
+  auto put = [&](int buf) {
+#pragma unroll
+    for (int i = 0; i < KC; ++i) {
+      const int e = ht + i * 256;
+      if (KX || e < C * N / 8) *(u32x4*)(Kl[buf] + Tile::at(e / (N / 8), (e % (N / 8)) * 8)) = xk[i];
     }
 #pragma unroll
     for (int i = 0; i < VC; ++i) {
       const int e = ht + i * 256;
       if (VX || e < C * VP) *(u32x4*)(Vl + (e / VP) * LV + (e % VP) * 8) = xv[i];
     }
-    if (ht < 3 * C) gl[buf][ht] = xg;
-  };
-
-  auto put_r = [&](int buf) {
 #pragma unroll
     for (int i = 0; i < RC; ++i) *(u32x4*)(Rl[buf] + (ht + i * 256) * 8) = xr[i];
+    if (ht < 3 * C) gl[buf][ht] = xg;
   };
   auto put_p = [&]() {
 #pragma unroll
@@ -280,59 +294,57 @@ __global__ __launch_bounds__(64 * NPT + 256, 1) void delta_fwd_kernel(DeltaArgs 
       if ((ht + i * 256) * 8 < EP) *(u32x4*)(Pl + (ht + i * 256) * 8) = xp[i];
   };
 
-  // qs: scale exp(G) (Q S^T)^T of the chunk last begun, qo of the one before it; uf: its U
-  f32x4 qs[4], qo[4];
-  Planes<2> uf[2];
-  auto take = [&]() {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) qo[i] = qs[i];
-#pragma unroll
-    for (int B = 0; B < 2; ++B)
-#pragma unroll
-      for (int m = 0; m < 2; ++m) uf[B].p[m] = as_bf16x8(Ux[tile][B][m][lane]);
-  };
-  // O of chunk c = qo + P U, stored with rows headdim: four elements of a token a lane
+  f32x4 qs[4];
+  // O of chunk c = scale exp(G) Q S^T (in qs) + P U, stored with rows headdim: four elements
+  // of a token a lane
   auto finish = [&](int c) {
+    const float* g = gl[(c - c0) & 1];
     bf16x8 pf[6];
+    f32x4 z[4];
+    Planes<2> uf[2];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) z[i] = *(const f32x4*)(g + 32 * (i >> 1) + 8 * q + 4 * (i & 1)) * Zx[tile][i][lane];
 #pragma unroll
     for (int i = 0; i < 6; ++i) pf[i] = as_bf16x8(*(const u32x4*)(Pl + i * 512 + lane * 8));
+#pragma unroll
+    for (int B = 0; B < 2; ++B) uf[B] = tile_planes<2>(z[2 * B], z[2 * B + 1]);
 #pragma unroll
     for (int m = 1; m >= 0; --m)
 #pragma unroll
       for (int S2 = 0; S2 < 2; ++S2)
 #pragma unroll
-        for (int i = 2 * S2; i < 4; ++i) qo[i] = mfma_bf16(uf[S2].p[m], pf[low_block(i >> 1, i & 1, S2)], qo[i]);
+        for (int i = 2 * S2; i < 4; ++i) qs[i] = mfma_bf16(uf[S2].p[m], pf[low_block(i >> 1, i & 1, S2)], qs[i]);
     const int start = sp.start + (c - c0) * C, len = min(C, sp.end - start);
     const uint32_t vrow = (uint32_t)a.H * a.P * 2;
     const brsrc ro = make_rsrc((char*)a.out + (((int64_t)start * a.H + h) * a.P + p0) * 2,
                                (uint32_t)(len - 1) * vrow + pw * 2);
 #pragma unroll
     for (int i = 0; i < 4; ++i)
-      store4io(ro, (32 * (i >> 1) + row32(r, i & 1)) * vrow + (16 * tile + 4 * q) * 2, qo[i], IoBf16{});
+      store4io(ro, (32 * (i >> 1) + row32(r, i & 1)) * vrow + (16 * tile + 4 * q) * 2, qs[i], IoBf16{});
   };
 
+  // (The loads run on to the last chunk again instead of stopping under a branch, at whose
+  // join they would be waited for.)
   if (c0 < c1) {
-    load_kqv(c0);
-    load_r(c0);
+    load(c0);
+    put(0);
+    load_q(c0);
     load_p(c0);
-    put_kqv(0);
-    put_r(0);
-    if (c0 + 1 < c1) {
-      load_kqv(c0 + 1);
-      load_r(c0 + 1);
-    }
+    load(min(c0 + 1, c1 - 1));
   }
-#pragma unroll
-  for (int i = 0; i < 4; ++i) qs[i] = zero;
   __syncthreads();
   for (int c = c0; c < c1; ++c) {
     // interval A
-    if (c > c0) {
-      put_p();  // of c - 1
-      load_p(c);
-    }
+    put_q();
+    load_q(min(c + 1, c1 - 1));
+    if (outs && c > c0) finish(c - 1);
+    __syncthreads();
+    // interval B
+    put((c + 1 - c0) & 1);
+    put_p();
+    load(min(c + 2, c1 - 1));
+    load_p(min(c + 1, c1 - 1));
     if (outs) {
-      if (c > c0) take();
       const float* g = gl[(c - c0) & 1];
 #pragma unroll
       for (int i = 0; i < 4; ++i) qs[i] = zero;
@@ -360,22 +372,8 @@ __global__ __launch_bounds__(64 * NPT + 256, 1) void delta_fwd_kernel(DeltaArgs 
       for (int i = 0; i < 4; ++i) qs[i] = (a.scale * g[C + 32 * (i >> 1) + row32(r, i & 1)]) * qs[i];
     }
     __syncthreads();
-    // interval B
-    if (c + 1 < c1) {
-      put_kqv((c + 1 - c0) & 1);
-      put_r((c + 1 - c0) & 1);
-      if (c + 2 < c1) {
-        load_kqv(c + 2);
-        load_r(c + 2);
-      }
-    }
-    if (outs && c > c0) finish(c - 1);
-    __syncthreads();
   }
-  if (c0 < c1) {
-    put_p();
-    if (outs) take();
-  }
+  // (the chain's last barrier: the last chunk's Z and P are there since the one before)
   __syncthreads();
   if (outs && c0 < c1) finish(c1 - 1);
 }

@@ -1,6 +1,8 @@
 // Gated delta rule, bf16 io, per chunk of 64 tokens and head: the running decay, and the
 // chunk matrices R = M (I + diag(b) M)^-1 with M = strict lower (K K^T . D), and
-// P = scale Q K^T . D (lower), as bf16 planes in the order the chains' operands take.
+// P = scale Q K^T . D (lower), as bf16 planes in the order the chains' operands take; R as
+// R diag(b) for the forward and (diag(b) R)^T for the backward, which saves the chains a
+// product with b on their way (the split is of the product, so nothing is rounded twice).
 //
 // One wave per (chunk, up to HPW heads of one group); waves do not interact.  K K^T and
 // Q K^T are computed transposed, so that a lane holds four (P: eight) consecutive
@@ -116,8 +118,11 @@ __global__ __launch_bounds__(256) void delta_prep_kernel(DeltaArgs a, int hpw, i
     gt[lane] = Gh;
     gt[C + lane] = Gl;
     gt[2 * C + lane] = bv;
-    gt[3 * C + lane] = exp2_hl(Gh, Gl);
-    gt[4 * C + lane] = exp2_fast((Ch - Gh) + (Cl - Gl));
+    const float eG = exp2_hl(Gh, Gl);
+    gt[3 * C + lane] = eG;
+    gt[4 * C + lane] = bv * exp2_fast((Ch - Gh) + (Cl - Gl));
+    gt[5 * C + lane] = exp2_fast((Ch - Gh) + (Cl - Gl));
+    gt[6 * C + lane] = bv * eG;
     __builtin_amdgcn_wave_barrier();
     gh[lane] = Gh;
     gl[lane] = Gl;
@@ -207,18 +212,21 @@ __global__ __launch_bounds__(256) void delta_prep_kernel(DeltaArgs a, int hpw, i
         for (int S = 0; S <= B; ++S)
 #pragma unroll
           for (int t = 0; t < 2; ++t) {
+            // forward R diag(b), backward (diag(b) R)^T
             const float* src = Rm + (32 * B + row32(r, t)) * kPrepLd + 32 * S + 8 * q;
+            const float* bc = bb + 32 * S + 8 * q;
             u32x4 o[2];
-            split8<2>(*(const f32x4*)src, *(const f32x4*)(src + 4), o);
+            split8<2>(*(const f32x4*)src * *(const f32x4*)bc, *(const f32x4*)(src + 4) * *(const f32x4*)(bc + 4), o);
 #pragma unroll
             for (int i = 0; i < 2; ++i) *(u32x4*)(dst + i * kTriPlane + low_block(B, t, S) * 512) = o[i];
             if constexpr (SAVE) {
               src = Rm + (32 * B + 8 * q) * kPrepLd + 32 * S + row32(r, t);
+              bc = bb + 32 * B + 8 * q;
               f32x4 x, y;
 #pragma unroll
               for (int e = 0; e < 4; ++e) {
-                x[e] = src[e * kPrepLd];
-                y[e] = src[(e + 4) * kPrepLd];
+                x[e] = bc[e] * src[e * kPrepLd];
+                y[e] = bc[e + 4] * src[(e + 4) * kPrepLd];
               }
               split8<2>(x, y, o);
 #pragma unroll
