@@ -30,10 +30,13 @@ __global__ __launch_bounds__(512) void delta_grads_kernel(DeltaArgs a) {
   constexpr int LN = N + 8, LP = PB + 8, LC = C + 8;  // rows: dstate; headdim; tokens
   constexpr int TN = N / 16, TH = (TN + 1) / 2;  // column tiles, of one half
   constexpr int SPL = PB * LN, UPL = PB * LC, OPL = C * LP, KPL = C * LN, CPL = C * LC;
-  constexpr int PH1 = 2 * PM * SPL + 2 * PM * UPL + PI * OPL, PH2 = 2 * PI * KPL + 2 * PM * CPL;
-  __shared__ __align__(16) uint16_t lds[PH1 > PH2 ? PH1 : PH2];
+  // bf16 io: K and Q stay in LDS over the heads; fp32 io: they share the states' place
+  constexpr bool KEEP = PI == 1;
+  constexpr int PH1 = 2 * PM * SPL + 2 * PM * UPL + PI * OPL, PH2 = 2 * PM * CPL + (KEEP ? 0 : 2 * PI * KPL);
+  __shared__ __align__(16) uint16_t lds[(PH1 > PH2 ? PH1 : PH2) + (KEEP ? 2 * PI * KPL : 0)];
   uint16_t *Sl = lds, *Dl = Sl + PM * SPL, *Ul = Dl + PM * SPL, *Xl = Ul + PM * UPL, *Ol = Xl + PM * UPL;
-  uint16_t *Kl = lds, *Ql = Kl + PI * KPL, *Pl = Ql + PI * KPL, *Ml = Pl + PM * CPL;
+  uint16_t *Pl = lds, *Ml = Pl + PM * CPL;
+  uint16_t *Kl = KEEP ? lds + (PH1 > PH2 ? PH1 : PH2) : Ml + PM * CPL, *Ql = Kl + PI * KPL;
   __shared__ __align__(16) float gl[3 * C];
   __shared__ float red[2][2][C], sd[NTH / 64], bsum[2][C];
 
@@ -50,21 +53,71 @@ __global__ __launch_bounds__(512) void delta_grads_kernel(DeltaArgs a) {
   const uint32_t vrow = (uint32_t)a.H * P * ES;
   const f32x4 zero = {0.f, 0.f, 0.f, 0.f};
 
+  auto put_kq = [&]() {
+    for (int e = tid; e < C * N / 8; e += NTH) {
+      const int t = e / (N / 8), col = (e % (N / 8)) * 8;
+      Raw8<IO> k8, q8;
+      k8.load(rk, t * krow + col * ES);
+      q8.load(rq, t * krow + col * ES);
+      u32x4 o[PI];
+      k8.planes(o);
+#pragma unroll
+      for (int m = 0; m < PI; ++m) *(u32x4*)(Kl + m * KPL + t * LN + col) = o[m];
+      q8.planes(o);
+#pragma unroll
+      for (int m = 0; m < PI; ++m) *(u32x4*)(Ql + m * KPL + t * LN + col) = o[m];
+    }
+  };
+  if constexpr (KEEP) put_kq();
+
+  // What a head (and block of headdim) needs from memory: the states (PB x N), Z and F
+  // (PB x 64) in tile order, dO (64 x PB), beta of this thread's tokens, the gates.  Loaded
+  // into registers while the one before is worked on, all through range-checked resources
+  // (past headdim they are zero).
+  constexpr int SE = PB * NP / 4, RE = PB * C / 4, OE = C * PB / 8;
+  constexpr int SC = (SE + NTH - 1) / NTH, RC = (RE + NTH - 1) / NTH;
+  static_assert(OE <= NTH && 3 * C <= NTH, "one piece a thread");
+  const int tk4 = 32 * ((w & 3) >> 1) + 8 * q + 4 * (w & 1);  // (a thread's tokens are the same in every tile)
+  const int ot = tid / (PB / 8), oc = (tid % (PB / 8)) * 8;
+  u32x4 xs[SC], xd[SC], xz[RC], xf_[RC], xb;
+  Raw8<IO> xo;
+  float xg;
+  auto scol = [&](int e) { return 32 * (((e >> 6) % (NP / 16)) >> 1) + 8 * q + 4 * ((e >> 6) & 1); };
+  auto load = [&](int hh, int pb) {
+    const int h = grp * per + hh;
+    const int64_t kh = (int64_t)ck * a.H + h;
+    const brsrc rs = make_rsrc(a.S + kh * P * NP, P * NP * 4), rd = make_rsrc(a.dS + kh * P * NP, P * NP * 4);
+#pragma unroll
+    for (int i = 0; i < SC; ++i) {
+      const int e = tid + i * NTH;
+      const uint32_t off = (SE % NTH == 0 || e < SE) && (N == NP || scol(e) < N) ? (pb * SE + e) * 16 : kNoOffset;
+      xs[i] = buf_load16(rs, off);
+      xd[i] = buf_load16(rd, off);
+    }
+    const brsrc rz = make_rsrc(a.Z + kh * C * P, C * P * 4), rf = make_rsrc(a.F + kh * C * P, C * P * 4);
+#pragma unroll
+    for (int i = 0; i < RC; ++i) {
+      const int e = tid + i * NTH;
+      xz[i] = buf_load16(rz, (pb * RE + e) * 16);
+      xf_[i] = buf_load16(rf, (pb * RE + e) * 16);
+    }
+    const brsrc ro = make_rsrc((const char*)a.dout + ((int64_t)start * a.H + h) * P * ES,
+                               (uint32_t)(len - 1) * vrow + P * ES);
+    xo.load(ro, tid < OE && pb * PB + oc < P ? ot * vrow + (pb * PB + oc) * ES : kNoOffset);
+    const brsrc rg = make_rsrc(a.gates + kh * kDeltaGates, 3 * C * 4);
+    xb = buf_load16(rg, (2 * C + tk4) * 4);
+    xg = buf_load_f32(rg, tid * 4);
+  };
+
   f32x4 dqs[TH], dks[TH];
 #pragma unroll
   for (int i = 0; i < TH; ++i) dqs[i] = dks[i] = zero;
 
+  load(0, 0);
+#pragma unroll 1
   for (int hh = 0; hh < per; ++hh) {
     const int h = grp * per + hh;
-    const int64_t kh = (int64_t)ck * a.H + h;
-    const f32x4* S = (const f32x4*)(a.S + kh * P * NP);
-    const f32x4* dS = (const f32x4*)(a.dS + kh * P * NP);
-    const f32x4* Z = (const f32x4*)(a.Z + kh * C * P);
-    const f32x4* F = (const f32x4*)(a.F + kh * C * P);
-    const brsrc ro = make_rsrc((const char*)a.dout + ((int64_t)start * a.H + h) * P * ES,
-                               (uint32_t)(len - 1) * vrow + P * ES);
     const brsrc rdv = make_rsrc((char*)a.dv + ((int64_t)start * a.H + h) * P * ES, (uint32_t)(len - 1) * vrow + P * ES);
-    if (tid < 3 * C) gl[tid] = a.gates[kh * kDeltaGates + tid];
     f32x4 dq[TH], dr[TH], dw[TH], cc[4];
 #pragma unroll
     for (int i = 0; i < TH; ++i) dq[i] = dr[i] = dw[i] = zero;
@@ -72,23 +125,14 @@ __global__ __launch_bounds__(512) void delta_grads_kernel(DeltaArgs a) {
     for (int i = 0; i < 4; ++i) cc[i] = zero;
     float sdot = 0.f;
     f32x4 bdot = zero;  // F . Z of four tokens, this thread's rows
-    const int tk4 = 32 * ((w & 3) >> 1) + 8 * q + 4 * (w & 1);
-    __syncthreads();
 #pragma unroll 1
     for (int pb = 0; pb < NB; ++pb) {
-      // stage the states (PB x N), Z and F as U and dX (PB x 64), and dO (64 x PB) as planes; a
-      // wave reads whole tiles (delta.hpp)
-      constexpr int SE = PB * NP / 4, RE = PB * C / 4;
-#pragma unroll 4
-      for (int e = tid; e < SE; e += NTH) {
-        const int tile = e >> 6, row = tile / (NP / 16) * 16 + r, col = 32 * ((tile % (NP / 16)) >> 1) + 8 * q + 4 * (tile & 1);
-        f32x4 x = zero, y = zero;
-        if (pb * PB + row < P && (N == NP || col < N)) {
-          x = S[pb * SE + e];
-          y = dS[pb * SE + e];
-        }
+#pragma unroll
+      for (int i = 0; i < SC; ++i) {
+        const int e = tid + i * NTH, row = (e >> 6) / (NP / 16) * 16 + r, col = scol(e);
+        const f32x4 x = __builtin_bit_cast(f32x4, xs[i]), y = __builtin_bit_cast(f32x4, xd[i]);
         sdot += x[0] * y[0] + x[1] * y[1] + x[2] * y[2] + x[3] * y[3];
-        if (N == NP || col < N) {
+        if ((SE % NTH == 0 || e < SE) && (N == NP || col < N)) {
           uint2 o[PM];
           split4<PM>(x, o);
 #pragma unroll
@@ -98,16 +142,12 @@ __global__ __launch_bounds__(512) void delta_grads_kernel(DeltaArgs a) {
           for (int m = 0; m < PM; ++m) *(uint2*)(Dl + m * SPL + row * LN + col) = o[m];
         }
       }
+      const f32x4 b = __builtin_bit_cast(f32x4, xb);
 #pragma unroll
-      for (int e = tid; e < RE; e += NTH) {  // (a thread's tokens are the same every time)
-        const int row = (e >> 8) * 16 + r;
-        f32x4 z = zero, f = zero;
-        if (pb * PB + row < P) {
-          z = Z[pb * RE + e];
-          f = F[pb * RE + e];
-        }
+      for (int i = 0; i < RC; ++i) {
+        const int e = tid + i * NTH, row = (e >> 8) * 16 + r;
+        const f32x4 z = __builtin_bit_cast(f32x4, xz[i]), f = __builtin_bit_cast(f32x4, xf_[i]);
         bdot += z * f;
-        const f32x4 b = *(const f32x4*)(gl + 2 * C + tk4);
         uint2 o[PM];
         split4<PM>(b * z, o);
 #pragma unroll
@@ -116,40 +156,46 @@ __global__ __launch_bounds__(512) void delta_grads_kernel(DeltaArgs a) {
 #pragma unroll
         for (int m = 0; m < PM; ++m) *(uint2*)(Xl + m * UPL + row * LC + tk4) = o[m];
       }
-      if (tid < C * PB / 8) {
-        const int t = tid / (PB / 8), col = (tid % (PB / 8)) * 8, p = pb * PB + col;
-        Raw8<IO> o8;
-        o8.load(ro, p < P ? t * vrow + p * ES : kNoOffset);
+      if (OE == NTH || tid < OE) {
         u32x4 o[PI];
-        o8.planes(o);
+        xo.planes(o);
 #pragma unroll
-        for (int m = 0; m < PI; ++m) *(u32x4*)(Ol + m * OPL + t * LP + col) = o[m];
+        for (int m = 0; m < PI; ++m) *(u32x4*)(Ol + m * OPL + ot * LP + oc) = o[m];
+      }
+      if (tid < 3 * C) gl[tid] = xg;
+      if constexpr (NB > 1) {
+        const int it = min(hh * NB + pb + 1, per * NB - 1);
+        load(it / NB, it % NB);
       }
       __syncthreads();
+      // (the lane, as the compiler cannot see it to be the same: operand addresses are formed
+      // anew in each phase rather than kept in registers over the heads)
+      int ln = lane;
+      asm("" : "+v"(ln));
 #pragma unroll 1
       for (int ks = 0; ks < PB / 32; ++ks) {
-        const Planes<PI> of = lds_rows<PI>(Ol + 16 * tb * LP + 32 * ks, LP, OPL, lane);
-        const Planes<PM> xf = lds_cols<PM>(Xl + 32 * ks * LC + 16 * tb, LC, UPL, lane);
-        const Planes<PM> uf = lds_cols<PM>(Ul + 32 * ks * LC + 16 * tb, LC, UPL, lane);
+        const Planes<PI> of = lds_rows<PI>(Ol + 16 * tb * LP + 32 * ks, LP, OPL, ln);
+        const Planes<PM> xf = lds_cols<PM>(Xl + 32 * ks * LC + 16 * tb, LC, UPL, ln);
+        const Planes<PM> uf = lds_cols<PM>(Ul + 32 * ks * LC + 16 * tb, LC, UPL, ln);
 #pragma unroll
         for (int i = 0; i < TH; ++i) {
           const int nt = nh * TH + i;
           if (nt < TN) {
-            const Planes<PM> sf = lds_cols<PM>(Sl + 32 * ks * LN + 16 * nt, LN, SPL, lane);
+            const Planes<PM> sf = lds_cols<PM>(Sl + 32 * ks * LN + 16 * nt, LN, SPL, ln);
             dq[i] = mma<PM>(sf, of, dq[i]);
             dr[i] = mma<PM>(sf, xf, dr[i]);
-            dw[i] = mma<PM>(lds_cols<PM>(Dl + 32 * ks * LN + 16 * nt, LN, SPL, lane), uf, dw[i]);
+            dw[i] = mma<PM>(lds_cols<PM>(Dl + 32 * ks * LN + 16 * nt, LN, SPL, ln), uf, dw[i]);
           }
         }
         // dX rounded to bf16 is its first plane: dV (the fp32 chain stores its own)
         if constexpr (PI == 1)
-          if (nh == 0 && pb * PB + 32 * ks + 8 * q < P)
-            buf_store16(rdv, tok * vrow + (pb * PB + 32 * ks + 8 * q) * ES, __builtin_bit_cast(u32x4, xf.p[0]));
+          if (nh == 0 && pb * PB + 32 * ks + 8 * (ln >> 4) < P)
+            buf_store16(rdv, (16 * tb + (ln & 15)) * vrow + (pb * PB + 32 * ks + 8 * (ln >> 4)) * ES, __builtin_bit_cast(u32x4, xf.p[0]));
         // rows j (block J), columns i: the first half dO U^T, the second dX U^T
 #pragma unroll
         for (int J = 0; J < 4; ++J)
           if (J <= tb) {
-            const Planes<PM> jf = lds_cols<PM>(Ul + 32 * ks * LC + 16 * J, LC, UPL, lane);
+            const Planes<PM> jf = lds_cols<PM>(Ul + 32 * ks * LC + 16 * J, LC, UPL, ln);
             cc[J] = nh == 0 ? mma<PM>(jf, of, cc[J]) : mma<PM>(jf, xf, cc[J]);
           }
       }
@@ -186,44 +232,40 @@ __global__ __launch_bounds__(512) void delta_grads_kernel(DeltaArgs a) {
         for (int m = 0; m < PM; ++m) *(uint2*)(dst + m * CPL + tok * LC + 16 * J + 4 * q) = o[m];
       }
     }
-    // K and Q
-    for (int e = tid; e < C * N / 8; e += NTH) {
-      const int t = e / (N / 8), col = (e % (N / 8)) * 8;
-      Raw8<IO> k8, q8;
-      k8.load(rk, t * krow + col * ES);
-      q8.load(rq, t * krow + col * ES);
-      u32x4 o[PI];
-      k8.planes(o);
-#pragma unroll
-      for (int m = 0; m < PI; ++m) *(u32x4*)(Kl + m * KPL + t * LN + col) = o[m];
-      q8.planes(o);
-#pragma unroll
-      for (int m = 0; m < PI; ++m) *(u32x4*)(Ql + m * KPL + t * LN + col) = o[m];
-    }
+    if constexpr (!KEEP) put_kq();
     __syncthreads();
+    // (one block of headdim: the next head's loads, where the registers of the first part are free)
+    if constexpr (NB == 1) load(min(hh + 1, per - 1), 0);
+    int l2 = lane;
+    asm("" : "+v"(l2));
+    const int q2 = l2 >> 4, t2 = 16 * tb + (l2 & 15);
     float da = 0.f, dwr = 0.f;  // this lane's part of dL/dG and of w
 #pragma unroll
     for (int i = 0; i < TH; ++i) {
       const int nt = nh * TH + i;
       if (nt < TN) {
-        Raw4<IO> k4, q4;
-        k4.load(rk, tok * krow + (16 * nt + 4 * q) * ES);
-        q4.load(rq, tok * krow + (16 * nt + 4 * q) * ES);
         const f32x4 w0 = dw[i];
 #pragma unroll
         for (int ks = 0; ks < 2; ++ks) {
-          const Planes<PI> kf = lds_cols<PI>(Kl + 32 * ks * LN + 16 * nt, LN, KPL, lane);
+          const Planes<PI> kf = lds_cols<PI>(Kl + 32 * ks * LN + 16 * nt, LN, KPL, l2);
           if (ks == 0 || tb >= 2) {  // i in this block, j up to it
-            dq[i] = mma<PM>(kf, lds_rows<PM>(Pl + 16 * tb * LC + 32 * ks, LC, CPL, lane), dq[i]);
-            dr[i] = mma<PM>(kf, lds_rows<PM>(Ml + 16 * tb * LC + 32 * ks, LC, CPL, lane), dr[i]);
+            dq[i] = mma<PM>(kf, lds_rows<PM>(Pl + 16 * tb * LC + 32 * ks, LC, CPL, l2), dq[i]);
+            dr[i] = mma<PM>(kf, lds_rows<PM>(Ml + 16 * tb * LC + 32 * ks, LC, CPL, l2), dr[i]);
           }
           if (ks == 1 || tb < 2) {  // j in this block, i from it on
-            const Planes<PI> qf = lds_cols<PI>(Ql + 32 * ks * LN + 16 * nt, LN, KPL, lane);
-            dw[i] = mma<PM>(qf, lds_cols<PM>(Pl + 32 * ks * LC + 16 * tb, LC, CPL, lane), dw[i]);
-            dw[i] = mma<PM>(kf, lds_cols<PM>(Ml + 32 * ks * LC + 16 * tb, LC, CPL, lane), dw[i]);
+            const Planes<PI> qf = lds_cols<PI>(Ql + 32 * ks * LN + 16 * nt, LN, KPL, l2);
+            dw[i] = mma<PM>(qf, lds_cols<PM>(Pl + 32 * ks * LC + 16 * tb, LC, CPL, l2), dw[i]);
+            dw[i] = mma<PM>(kf, lds_cols<PM>(Ml + 32 * ks * LC + 16 * tb, LC, CPL, l2), dw[i]);
           }
         }
-        const f32x4 kv = k4.get(), qv = q4.get();
+        f32x4 kv = zero, qv = zero;  // (planes add up to the input exactly)
+#pragma unroll
+        for (int m = PI - 1; m >= 0; --m) {
+          const uint2 kw = *(const uint2*)(Kl + m * KPL + t2 * LN + 16 * nt + 4 * q2);
+          const uint2 qw = *(const uint2*)(Ql + m * KPL + t2 * LN + 16 * nt + 4 * q2);
+          kv += f32x4{bf_lo(kw.x), bf_hi(kw.x), bf_lo(kw.y), bf_hi(kw.y)};
+          qv += f32x4{bf_lo(qw.x), bf_hi(qw.x), bf_lo(qw.y), bf_hi(qw.y)};
+        }
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           da += qv[e] * dq[i][e] + kv[e] * (dr[i][e] - (dw[i][e] - w0[e]));
@@ -271,8 +313,7 @@ __global__ __launch_bounds__(512) void delta_grads_kernel(DeltaArgs a) {
         a.dbeta[at] = bsum[0][lane] + bsum[1][lane];
       }
     }
-    // (the next head's first barrier is behind these reads: gl is rewritten before it)
-    __syncthreads();
+    __syncthreads();  // (the next head's data goes where P, M and the gates are)
   }
   const brsrc wq = make_rsrc((char*)a.dq + kbase, kspan), wk = make_rsrc((char*)a.dk + kbase, kspan);
 #pragma unroll
