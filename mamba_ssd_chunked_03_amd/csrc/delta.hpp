@@ -184,6 +184,11 @@ __device__ __forceinline__ Planes<NP> lds_cols(const uint16_t* t, int ld, int pl
   return f;
 }
 
+// 16-byte load at a vector and a scalar offset
+__device__ __forceinline__ u32x4 buf_load16(brsrc r, uint32_t off, int soff) {
+  return __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(r, off, soff, 0));
+}
+
 // An io row's 8 elements as raw 16-byte pieces (one for bf16, two for fp32), loaded
 // through a range-checked resource, and their planes.
 template <class IO>

@@ -13,9 +13,11 @@
 // w_j enters dg_i as the sum over j < i and exp(G_C) <S, dS> alone is carried, instead of
 // two large sums that cancel.  dg is the suffix sum of dL/dG within the chunk.
 //
-// dq and dk are summed over the group's heads in registers, in order.  Eight waves: wave
-// w has tokens 16 (w % 4).. and one half of the N columns (w / 4); dP, dM are formed by
-// the two halves.
+// dq and dk are summed over the group's heads in registers, in order.  Eight waves: wave w
+// has tokens 32 (w % 2)..+31 and a quarter (w / 2) of the N columns, which reads each
+// operand from LDS two to four times (16 tokens and half the columns a wave: 1.3 times as
+// much); 16 rows of dP (first four waves) or dM (last four).  The running sums of a head's
+// gates are formed by one wave while the others begin the next head.
 #include "delta.hpp"
 
 namespace ssd {
@@ -28,7 +30,7 @@ __global__ __launch_bounds__(512) void delta_grads_kernel(DeltaArgs a) {
   // columns of headdim staged at a time (the products' depth is 32; past P they are zero)
   constexpr int PB = P < 32 ? 32 : (P > (PM == 2 ? 64 : 32) ? (PM == 2 ? 64 : 32) : P), NB = (P + PB - 1) / PB;
   constexpr int LN = N + 8, LP = PB + 8, LC = C + 8;  // rows: dstate; headdim; tokens
-  constexpr int TN = N / 16, TH = (TN + 1) / 2;  // column tiles, of one half
+  constexpr int TN = N / 16, TQ = (TN + 3) / 4;  // column tiles, of one quarter
   constexpr int SPL = PB * LN, UPL = PB * LC, OPL = C * LP, KPL = C * LN, CPL = C * LC;
   // bf16 io: K and Q stay in LDS over the heads; fp32 io: they share the states' place
   constexpr bool KEEP = PI == 1;
@@ -37,11 +39,12 @@ __global__ __launch_bounds__(512) void delta_grads_kernel(DeltaArgs a) {
   uint16_t *Sl = lds, *Dl = Sl + PM * SPL, *Ul = Dl + PM * SPL, *Xl = Ul + PM * UPL, *Ol = Xl + PM * UPL;
   uint16_t *Pl = lds, *Ml = Pl + PM * CPL;
   uint16_t *Kl = KEEP ? lds + (PH1 > PH2 ? PH1 : PH2) : Ml + PM * CPL, *Ql = Kl + PI * KPL;
+  // gates; row dots (of G and of w) of the four quarters; parts of <S, dS> and exp(G_C); parts of dbeta
   __shared__ __align__(16) float gl[3 * C];
-  __shared__ float red[2][2][C], sd[NTH / 64], bsum[2][C];
+  __shared__ float red[2][4][C], sd[NTH / 64 + 1], bsum[2][C];
 
   const int tid = threadIdx.x, w = __builtin_amdgcn_readfirstlane(tid >> 6), lane = tid & 63, q = lane >> 4, r = lane & 15;
-  const int tb = w & 3, nh = w >> 2, tok = 16 * tb + r;
+  const int tp = w & 1, nq = w >> 1, tb = w & 3, md = w >> 2;
   const int wg = xcd_order(blockIdx.x, gridDim.x);
   const int ck = wg / a.G, grp = wg % a.G, per = a.H / a.G;
   ChunkInfo ci = chunk_info(a.map, ck);
@@ -75,94 +78,125 @@ __global__ __launch_bounds__(512) void delta_grads_kernel(DeltaArgs a) {
   // into registers while the one before is worked on, all through range-checked resources
   // (past headdim they are zero).
   constexpr int SE = PB * NP / 4, RE = PB * C / 4, OE = C * PB / 8;
-  constexpr int SC = (SE + NTH - 1) / NTH, RC = (RE + NTH - 1) / NTH;
-  static_assert(OE <= NTH && 3 * C <= NTH, "one piece a thread");
-  const int tk4 = 32 * ((w & 3) >> 1) + 8 * q + 4 * (w & 1);  // (a thread's tokens are the same in every tile)
-  const int ot = tid / (PB / 8), oc = (tid % (PB / 8)) * 8;
+  constexpr int SC = (SE + NTH - 1) / NTH, RC = (RE + NTH - 1) / NTH, TPR = NP / 16;
+  static_assert(OE <= NTH && 3 * C <= NTH && RE % NTH == 0, "pieces of a thread");
+  // wave w's tile i of the states: rows 16 (i 8 / TPR + w / TPR).., column tile w % TPR; of Z
+  // and F: rows 16 (2i + w / 4).., token tile w % 4
+  const int tk4 = 32 * ((w & 3) >> 1) + 8 * q + 4 * (w & 1);  // (the same tokens in each)
+  const int scol = 32 * ((w % TPR) >> 1) + 8 * q + 4 * (w & 1);
   u32x4 xs[SC], xd[SC], xz[RC], xf_[RC], xb;
   Raw8<IO> xo;
   float xg;
-  auto scol = [&](int e) { return 32 * (((e >> 6) % (NP / 16)) >> 1) + 8 * q + 4 * ((e >> 6) & 1); };
   auto load = [&](int hh, int pb) {
     const int h = grp * per + hh;
     const int64_t kh = (int64_t)ck * a.H + h;
+    int td = tid;  // (not seen to be the same: the offsets are formed anew)
+    asm("" : "+v"(td));
     const brsrc rs = make_rsrc(a.S + kh * P * NP, P * NP * 4), rd = make_rsrc(a.dS + kh * P * NP, P * NP * 4);
 #pragma unroll
     for (int i = 0; i < SC; ++i) {
-      const int e = tid + i * NTH;
-      const uint32_t off = (SE % NTH == 0 || e < SE) && (N == NP || scol(e) < N) ? (pb * SE + e) * 16 : kNoOffset;
-      xs[i] = buf_load16(rs, off);
-      xd[i] = buf_load16(rd, off);
+      const uint32_t off = (SE % NTH == 0 || td + i * NTH < SE) && (N == NP || scol < N) ? td * 16 : kNoOffset;
+      xs[i] = buf_load16(rs, off, (pb * SE + i * NTH) * 16);
+      xd[i] = buf_load16(rd, off, (pb * SE + i * NTH) * 16);
     }
     const brsrc rz = make_rsrc(a.Z + kh * C * P, C * P * 4), rf = make_rsrc(a.F + kh * C * P, C * P * 4);
 #pragma unroll
     for (int i = 0; i < RC; ++i) {
-      const int e = tid + i * NTH;
-      xz[i] = buf_load16(rz, (pb * RE + e) * 16);
-      xf_[i] = buf_load16(rf, (pb * RE + e) * 16);
+      xz[i] = buf_load16(rz, td * 16, (pb * RE + i * NTH) * 16);
+      xf_[i] = buf_load16(rf, td * 16, (pb * RE + i * NTH) * 16);
     }
     const brsrc ro = make_rsrc((const char*)a.dout + ((int64_t)start * a.H + h) * P * ES,
                                (uint32_t)(len - 1) * vrow + P * ES);
-    xo.load(ro, tid < OE && pb * PB + oc < P ? ot * vrow + (pb * PB + oc) * ES : kNoOffset);
+    const int ot = td / (PB / 8), oc = pb * PB + (td % (PB / 8)) * 8;
+    xo.load(ro, td < OE && oc < P ? ot * vrow + oc * ES : kNoOffset);
     const brsrc rg = make_rsrc(a.gates + kh * kDeltaGates, 3 * C * 4);
     xb = buf_load16(rg, (2 * C + tk4) * 4);
-    xg = buf_load_f32(rg, tid * 4);
+    xg = buf_load_f32(rg, td * 4);
   };
 
-  f32x4 dqs[TH], dks[TH];
+  f32x4 dqs[2][TQ], dks[2][TQ];
 #pragma unroll
-  for (int i = 0; i < TH; ++i) dqs[i] = dks[i] = zero;
+  for (int b = 0; b < 2; ++b)
+#pragma unroll
+    for (int i = 0; i < TQ; ++i) dqs[b][i] = dks[b][i] = zero;
+  // dg and dbeta of a head from its parts in LDS (one wave)
+  auto gates = [&](int hh) {
+    float t = 0.f;
+#pragma unroll
+    for (int i = 0; i < NTH / 64; ++i) t += sd[i];
+    // suffix sums with the tokens in reverse over the lanes, prefix sums in order
+    int lane = tid & 63;
+    asm("" : "+v"(lane));
+    const int rl = C - 1 - lane;
+    float x = (red[0][0][rl] + red[0][1][rl]) + (red[0][2][rl] + red[0][3][rl]);
+    if (lane == 0) x += sd[NTH / 64] * t;
+    const float wj = (red[1][0][lane] + red[1][1][lane]) + (red[1][2][lane] + red[1][3][lane]);
+    x = wave_inclusive_sum(x);
+    const float y = wave_inclusive_sum(wj) - wj;
+    x = __shfl(x, rl);
+    if (lane < len) {
+      const int64_t at = ((int64_t)start + lane) * a.H + grp * per + hh;
+      a.dg[at] = x + y;
+      a.dbeta[at] = bsum[0][lane] + bsum[1][lane];
+    }
+  };
 
   load(0, 0);
 #pragma unroll 1
   for (int hh = 0; hh < per; ++hh) {
     const int h = grp * per + hh;
     const brsrc rdv = make_rsrc((char*)a.dv + ((int64_t)start * a.H + h) * P * ES, (uint32_t)(len - 1) * vrow + P * ES);
-    f32x4 dq[TH], dr[TH], dw[TH], cc[4];
+    f32x4 dq[2][TQ], dr[2][TQ], dw[2][TQ], cc[4];
 #pragma unroll
-    for (int i = 0; i < TH; ++i) dq[i] = dr[i] = dw[i] = zero;
+    for (int b = 0; b < 2; ++b)
+#pragma unroll
+      for (int i = 0; i < TQ; ++i) dq[b][i] = dr[b][i] = dw[b][i] = zero;
 #pragma unroll
     for (int i = 0; i < 4; ++i) cc[i] = zero;
     float sdot = 0.f;
     f32x4 bdot = zero;  // F . Z of four tokens, this thread's rows
 #pragma unroll 1
     for (int pb = 0; pb < NB; ++pb) {
+      int td = tid;
+      asm("" : "+v"(td));
+      const int lr = td & 15;
 #pragma unroll
       for (int i = 0; i < SC; ++i) {
-        const int e = tid + i * NTH, row = (e >> 6) / (NP / 16) * 16 + r, col = scol(e);
+        const int at = (16 * (i * (8 / TPR) + w / TPR) + lr) * LN + scol;
         const f32x4 x = __builtin_bit_cast(f32x4, xs[i]), y = __builtin_bit_cast(f32x4, xd[i]);
         sdot += x[0] * y[0] + x[1] * y[1] + x[2] * y[2] + x[3] * y[3];
-        if ((SE % NTH == 0 || e < SE) && (N == NP || col < N)) {
+        if ((SE % NTH == 0 || td + i * NTH < SE) && (N == NP || scol < N)) {
           uint2 o[PM];
           split4<PM>(x, o);
 #pragma unroll
-          for (int m = 0; m < PM; ++m) *(uint2*)(Sl + m * SPL + row * LN + col) = o[m];
+          for (int m = 0; m < PM; ++m) *(uint2*)(Sl + m * SPL + at) = o[m];
           split4<PM>(y, o);
 #pragma unroll
-          for (int m = 0; m < PM; ++m) *(uint2*)(Dl + m * SPL + row * LN + col) = o[m];
+          for (int m = 0; m < PM; ++m) *(uint2*)(Dl + m * SPL + at) = o[m];
         }
       }
       const f32x4 b = __builtin_bit_cast(f32x4, xb);
 #pragma unroll
       for (int i = 0; i < RC; ++i) {
-        const int e = tid + i * NTH, row = (e >> 8) * 16 + r;
+        const int at = (16 * (2 * i + (w >> 2)) + lr) * LC + tk4;
         const f32x4 z = __builtin_bit_cast(f32x4, xz[i]), f = __builtin_bit_cast(f32x4, xf_[i]);
         bdot += z * f;
         uint2 o[PM];
         split4<PM>(b * z, o);
 #pragma unroll
-        for (int m = 0; m < PM; ++m) *(uint2*)(Ul + m * UPL + row * LC + tk4) = o[m];
+        for (int m = 0; m < PM; ++m) *(uint2*)(Ul + m * UPL + at) = o[m];
         split4<PM>(b * f, o);
 #pragma unroll
-        for (int m = 0; m < PM; ++m) *(uint2*)(Xl + m * UPL + row * LC + tk4) = o[m];
+        for (int m = 0; m < PM; ++m) *(uint2*)(Xl + m * UPL + at) = o[m];
       }
-      if (OE == NTH || tid < OE) {
+      if (OE == NTH || td < OE) {
         u32x4 o[PI];
         xo.planes(o);
 #pragma unroll
-        for (int m = 0; m < PI; ++m) *(u32x4*)(Ol + m * OPL + ot * LP + oc) = o[m];
+        for (int m = 0; m < PI; ++m) *(u32x4*)(Ol + m * OPL + td / (PB / 8) * LP + (td % (PB / 8)) * 8) = o[m];
       }
       if (tid < 3 * C) gl[tid] = xg;
+      if (pb == 0 && hh > 0 && w == (hh & 7)) gates(hh - 1);
       if constexpr (NB > 1) {
         const int it = min(hh * NB + pb + 1, per * NB - 1);
         load(it / NB, it % NB);
@@ -174,46 +208,68 @@ __global__ __launch_bounds__(512) void delta_grads_kernel(DeltaArgs a) {
       asm("" : "+v"(ln));
 #pragma unroll 1
       for (int ks = 0; ks < PB / 32; ++ks) {
-        const Planes<PI> of = lds_rows<PI>(Ol + 16 * tb * LP + 32 * ks, LP, OPL, ln);
-        const Planes<PM> xf = lds_cols<PM>(Xl + 32 * ks * LC + 16 * tb, LC, UPL, ln);
-        const Planes<PM> uf = lds_cols<PM>(Ul + 32 * ks * LC + 16 * tb, LC, UPL, ln);
+        Planes<PI> of[2];
+        Planes<PM> xf[2], uf[2];
 #pragma unroll
-        for (int i = 0; i < TH; ++i) {
-          const int nt = nh * TH + i;
-          if (nt < TN) {
+        for (int b = 0; b < 2; ++b) {
+          of[b] = lds_rows<PI>(Ol + 16 * (2 * tp + b) * LP + 32 * ks, LP, OPL, ln);
+          xf[b] = lds_cols<PM>(Xl + 32 * ks * LC + 16 * (2 * tp + b), LC, UPL, ln);
+          uf[b] = lds_cols<PM>(Ul + 32 * ks * LC + 16 * (2 * tp + b), LC, UPL, ln);
+        }
+#pragma unroll
+        for (int i = 0; i < TQ; ++i) {
+          const int nt = nq * TQ + i;
+          if (TN % 4 == 0 || nt < TN) {
             const Planes<PM> sf = lds_cols<PM>(Sl + 32 * ks * LN + 16 * nt, LN, SPL, ln);
-            dq[i] = mma<PM>(sf, of, dq[i]);
-            dr[i] = mma<PM>(sf, xf, dr[i]);
-            dw[i] = mma<PM>(lds_cols<PM>(Dl + 32 * ks * LN + 16 * nt, LN, SPL, ln), uf, dw[i]);
+            const Planes<PM> df = lds_cols<PM>(Dl + 32 * ks * LN + 16 * nt, LN, SPL, ln);
+#pragma unroll
+            for (int b = 0; b < 2; ++b) {
+              dq[b][i] = mma<PM>(sf, of[b], dq[b][i]);
+              dr[b][i] = mma<PM>(sf, xf[b], dr[b][i]);
+              dw[b][i] = mma<PM>(df, uf[b], dw[b][i]);
+            }
           }
         }
         // dX rounded to bf16 is its first plane: dV (the fp32 chain stores its own)
-        if constexpr (PI == 1)
-          if (nh == 0 && pb * PB + 32 * ks + 8 * (ln >> 4) < P)
-            buf_store16(rdv, (16 * tb + (ln & 15)) * vrow + (pb * PB + 32 * ks + 8 * (ln >> 4)) * ES, __builtin_bit_cast(u32x4, xf.p[0]));
-        // rows j (block J), columns i: the first half dO U^T, the second dX U^T
+        if constexpr (PI == 1) {
+          const int p = pb * PB + 32 * ks + 8 * (ln >> 4);
+          if (nq == 0 && p < P)
+#pragma unroll
+            for (int b = 0; b < 2; ++b)
+              buf_store16(rdv, (16 * (2 * tp + b) + (ln & 15)) * vrow + p * ES, __builtin_bit_cast(u32x4, xf[b].p[0]));
+        }
+        // rows j (block J) of dO U^T or dX U^T, columns i (block tb)
 #pragma unroll
         for (int J = 0; J < 4; ++J)
           if (J <= tb) {
             const Planes<PM> jf = lds_cols<PM>(Ul + 32 * ks * LC + 16 * J, LC, UPL, ln);
-            cc[J] = nh == 0 ? mma<PM>(jf, of, cc[J]) : mma<PM>(jf, xf, cc[J]);
+            if (md == 0)
+              cc[J] = mma<PM>(jf, lds_rows<PI>(Ol + 16 * tb * LP + 32 * ks, LP, OPL, ln), cc[J]);
+            else
+              cc[J] = mma<PM>(jf, lds_cols<PM>(Xl + 32 * ks * LC + 16 * tb, LC, UPL, ln), cc[J]);
           }
       }
       __syncthreads();
     }
-    const float Gh = gl[tok], Gl = gl[C + tok];
-    const float eG = exp2_hl(Gh, Gl), eR = exp2_fast((gl[C - 1] - Gh) + (gl[2 * C - 1] - Gl));
 #pragma unroll
-    for (int i = 0; i < TH; ++i) {
-      dq[i] = (a.scale * eG) * dq[i];
-      dr[i] = -eG * dr[i];
-      dw[i] = eR * dw[i];
+    for (int b = 0; b < 2; ++b) {
+      const int tok = 16 * (2 * tp + b) + r;
+      const float Gh = gl[tok], Gl = gl[C + tok];
+      const float eG = exp2_hl(Gh, Gl), eR = exp2_fast((gl[C - 1] - Gh) + (gl[2 * C - 1] - Gl));
+#pragma unroll
+      for (int i = 0; i < TQ; ++i) {
+        dq[b][i] = (a.scale * eG) * dq[b][i];
+        dr[b][i] = -eG * dr[b][i];
+        dw[b][i] = eR * dw[b][i];
+      }
     }
-    // dP (first half) or dM (second), [i][j]; the block right of an even diagonal one is read
-    // in the same step of 32 and written as zero
+    // dP or dM, [i][j]; the block right of an even diagonal one is read in the same step of 32
+    // and written as zero
     {
-      uint16_t* dst = nh == 0 ? Pl : Ml;
-      const float f = nh == 0 ? a.scale : -1.f;
+      uint16_t* dst = md == 0 ? Pl : Ml;
+      const float f = md == 0 ? a.scale : -1.f;
+      const int tok = 16 * tb + r;
+      const float Gh = gl[tok], Gl = gl[C + tok];
 #pragma unroll
       for (int J = 0; J < 4; ++J) {
         if (J > tb && !(J == tb + 1 && (tb & 1) == 0)) continue;
@@ -223,7 +279,7 @@ __global__ __launch_bounds__(512) void delta_grads_kernel(DeltaArgs a) {
           for (int e = 0; e < 4; ++e) {
             const int j = 16 * J + 4 * q + e;
             const float d = exp2_fast((Gh - gl[j]) + (Gl - gl[C + j]));
-            v[e] = (nh == 0 ? j <= tok : j < tok) ? f * (cc[J][e] * d) : 0.f;
+            v[e] = (md == 0 ? j <= tok : j < tok) ? f * (cc[J][e] * d) : 0.f;
           }
         }
         uint2 o[PM];
@@ -238,92 +294,105 @@ __global__ __launch_bounds__(512) void delta_grads_kernel(DeltaArgs a) {
     if constexpr (NB == 1) load(min(hh + 1, per - 1), 0);
     int l2 = lane;
     asm("" : "+v"(l2));
-    const int q2 = l2 >> 4, t2 = 16 * tb + (l2 & 15);
-    float da = 0.f, dwr = 0.f;  // this lane's part of dL/dG and of w
+    const int q2 = l2 >> 4, r2 = l2 & 15;
+    // k and q of a tile's token and columns (planes add up to the input exactly)
+    auto value = [&](const uint16_t* X, int tok, int nt) {
+      f32x4 v = zero;
 #pragma unroll
-    for (int i = 0; i < TH; ++i) {
-      const int nt = nh * TH + i;
-      if (nt < TN) {
-        const f32x4 w0 = dw[i];
-#pragma unroll
-        for (int ks = 0; ks < 2; ++ks) {
-          const Planes<PI> kf = lds_cols<PI>(Kl + 32 * ks * LN + 16 * nt, LN, KPL, l2);
-          if (ks == 0 || tb >= 2) {  // i in this block, j up to it
-            dq[i] = mma<PM>(kf, lds_rows<PM>(Pl + 16 * tb * LC + 32 * ks, LC, CPL, l2), dq[i]);
-            dr[i] = mma<PM>(kf, lds_rows<PM>(Ml + 16 * tb * LC + 32 * ks, LC, CPL, l2), dr[i]);
-          }
-          if (ks == 1 || tb < 2) {  // j in this block, i from it on
-            const Planes<PI> qf = lds_cols<PI>(Ql + 32 * ks * LN + 16 * nt, LN, KPL, l2);
-            dw[i] = mma<PM>(qf, lds_cols<PM>(Pl + 32 * ks * LC + 16 * tb, LC, CPL, l2), dw[i]);
-            dw[i] = mma<PM>(kf, lds_cols<PM>(Ml + 32 * ks * LC + 16 * tb, LC, CPL, l2), dw[i]);
-          }
-        }
-        f32x4 kv = zero, qv = zero;  // (planes add up to the input exactly)
-#pragma unroll
-        for (int m = PI - 1; m >= 0; --m) {
-          const uint2 kw = *(const uint2*)(Kl + m * KPL + t2 * LN + 16 * nt + 4 * q2);
-          const uint2 qw = *(const uint2*)(Ql + m * KPL + t2 * LN + 16 * nt + 4 * q2);
-          kv += f32x4{bf_lo(kw.x), bf_hi(kw.x), bf_lo(kw.y), bf_hi(kw.y)};
-          qv += f32x4{bf_lo(qw.x), bf_hi(qw.x), bf_lo(qw.y), bf_hi(qw.y)};
-        }
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          da += qv[e] * dq[i][e] + kv[e] * (dr[i][e] - (dw[i][e] - w0[e]));
-          dwr += kv[e] * w0[e];
-        }
-        dqs[i] += dq[i];
-        dks[i] += dr[i] + dw[i];
+      for (int m = PI - 1; m >= 0; --m) {
+        const uint2 x = *(const uint2*)(X + m * KPL + tok * LN + 16 * nt + 4 * q2);
+        v += f32x4{bf_lo(x.x), bf_hi(x.x), bf_lo(x.y), bf_hi(x.y)};
       }
-    }
-    da += __shfl_xor(da, 16);
-    da += __shfl_xor(da, 32);
-    dwr += __shfl_xor(dwr, 16);
-    dwr += __shfl_xor(dwr, 32);
-    if (q == 0) {
-      red[0][nh][tok] = da;
-      red[1][nh][tok] = dwr;
+      return v;
+    };
+    float dwr[2] = {0.f, 0.f};  // this lane's part of w
+    __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+    for (int b = 0; b < 2; ++b)
+#pragma unroll
+      for (int i = 0; i < TQ; ++i)
+        if (TN % 4 == 0 || nq * TQ + i < TN) {
+          const f32x4 kv = value(Kl, 16 * (2 * tp + b) + r2, nq * TQ + i);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) dwr[b] += kv[e] * dw[b][i][e];
+        }
+    // (one block of tokens at a time, in parts that the scheduler keeps apart: registers)
+#pragma unroll
+    for (int ks = 0; ks < 2; ++ks)
+#pragma unroll
+      for (int b = 0; b < 2; ++b) {
+        const int t0 = 16 * (2 * tp + b);
+        if (ks == 0 || tp == 1) {  // j in this block, up to i
+          const Planes<PM> pr = lds_rows<PM>(Pl + t0 * LC + 32 * ks, LC, CPL, l2);
+          const Planes<PM> mr = lds_rows<PM>(Ml + t0 * LC + 32 * ks, LC, CPL, l2);
+#pragma unroll
+          for (int i = 0; i < TQ; ++i)
+            if (TN % 4 == 0 || nq * TQ + i < TN) {
+              const Planes<PI> kf = lds_cols<PI>(Kl + 32 * ks * LN + 16 * (nq * TQ + i), LN, KPL, l2);
+              dq[b][i] = mma<PM>(kf, pr, dq[b][i]);
+              dr[b][i] = mma<PM>(kf, mr, dr[b][i]);
+            }
+        }
+        if (ks == 1 || tp == 0) {  // i in this block, from j on
+          const Planes<PM> pc = lds_cols<PM>(Pl + 32 * ks * LC + t0, LC, CPL, l2);
+          const Planes<PM> mc = lds_cols<PM>(Ml + 32 * ks * LC + t0, LC, CPL, l2);
+#pragma unroll
+          for (int i = 0; i < TQ; ++i)
+            if (TN % 4 == 0 || nq * TQ + i < TN) {
+              const Planes<PI> kf = lds_cols<PI>(Kl + 32 * ks * LN + 16 * (nq * TQ + i), LN, KPL, l2);
+              const Planes<PI> qf = lds_cols<PI>(Ql + 32 * ks * LN + 16 * (nq * TQ + i), LN, KPL, l2);
+              dw[b][i] = mma<PM>(qf, pc, dw[b][i]);
+              dw[b][i] = mma<PM>(kf, mc, dw[b][i]);
+            }
+        }
+        __builtin_amdgcn_sched_barrier(0);
+      }
+#pragma unroll
+    for (int b = 0; b < 2; ++b) {
+      const int tok = 16 * (2 * tp + b) + r2;
+      float da = dwr[b];  // this lane's part of dL/dG
+#pragma unroll
+      for (int i = 0; i < TQ; ++i)
+        if (TN % 4 == 0 || nq * TQ + i < TN) {
+          const f32x4 kv = value(Kl, tok, nq * TQ + i), qv = value(Ql, tok, nq * TQ + i);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) da += qv[e] * dq[b][i][e] + kv[e] * (dr[b][i][e] - dw[b][i][e]);
+          dqs[b][i] += dq[b][i];
+          dks[b][i] += dr[b][i] + dw[b][i];
+        }
+      da += __shfl_xor(da, 16);
+      da += __shfl_xor(da, 32);
+      dwr[b] += __shfl_xor(dwr[b], 16);
+      dwr[b] += __shfl_xor(dwr[b], 32);
+      if (q == 0) {
+        red[0][nq][tok] = da;
+        red[1][nq][tok] = dwr[b];
+      }
     }
     sdot = wave_sum(sdot);
     if (lane == 0) sd[w] = sdot;
+    if (tid == 0) sd[NTH / 64] = exp2_hl(gl[C - 1], gl[2 * C - 1]);
     // F . Z over the rows: 16 lanes, then two waves in order
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
       const float v = row_sum16(bdot[e]);
       if (r == 0) bsum[w >> 2][tk4 + e] = v;
     }
-    __syncthreads();
-    if (w == 0) {
-      double x = (double)red[0][0][lane] + (double)red[0][1][lane];
-      double y = (double)red[1][0][lane] + (double)red[1][1][lane];
-      const double wj = y;
-      if (lane == C - 1) {
-        float t = 0.f;
-        for (int i = 0; i < NTH / 64; ++i) t += sd[i];
-        x += (double)(exp2_hl(gl[C - 1], gl[2 * C - 1]) * t);
-      }
-#pragma unroll
-      for (int d = 1; d < 64; d <<= 1) {
-        const double u = __shfl_down(x, d), v = __shfl_up(y, d);
-        if (lane + d < 64) x += u;
-        if (lane >= d) y += v;
-      }
-      if (lane < len) {
-        const int64_t at = ((int64_t)start + lane) * a.H + h;
-        a.dg[at] = (float)(x + (y - wj));
-        a.dbeta[at] = bsum[0][lane] + bsum[1][lane];
-      }
-    }
-    __syncthreads();  // (the next head's data goes where P, M and the gates are)
+    __syncthreads();  // (the next head's data goes where P and M are)
   }
+  if (w == 0) gates(per - 1);
   const brsrc wq = make_rsrc((char*)a.dq + kbase, kspan), wk = make_rsrc((char*)a.dk + kbase, kspan);
 #pragma unroll
-  for (int i = 0; i < TH; ++i) {
-    const int nt = nh * TH + i;
-    if (nt < TN) {
-      store4io(wq, tok * krow + (16 * nt + 4 * q) * ES, dqs[i], IO{});
-      store4io(wk, tok * krow + (16 * nt + 4 * q) * ES, dks[i], IO{});
+  for (int b = 0; b < 2; ++b)
+#pragma unroll
+    for (int i = 0; i < TQ; ++i) {
+      const int nt = nq * TQ + i;
+      if (TN % 4 == 0 || nt < TN) {
+        const uint32_t off = (16 * (2 * tp + b) + r) * krow + (16 * nt + 4 * q) * ES;
+        store4io(wq, off, dqs[b][i], IO{});
+        store4io(wk, off, dks[b][i], IO{});
+      }
     }
-  }
 }
 
 hipError_t launch_delta_bwd_grads(const DeltaProb& p, const DeltaArgs& a, hipStream_t st) {
