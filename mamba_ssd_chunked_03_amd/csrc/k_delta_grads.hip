@@ -87,10 +87,9 @@ __global__ __launch_bounds__(512) void delta_grads_kernel(DeltaArgs a) {
   u32x4 xs[SC], xd[SC], xz[RC], xf_[RC], xb;
   Raw8<IO> xo;
   float xg;
-  auto load = [&](int hh, int pb) {
-    const int h = grp * per + hh;
-    const int64_t kh = (int64_t)ck * a.H + h;
-    int td = tid;  // (not seen to be the same: the offsets are formed anew)
+  auto load_s = [&](int hh, int pb) {
+    const int64_t kh = (int64_t)ck * a.H + grp * per + hh;
+    int td = tid;
     asm("" : "+v"(td));
     const brsrc rs = make_rsrc(a.S + kh * P * NP, P * NP * 4), rd = make_rsrc(a.dS + kh * P * NP, P * NP * 4);
 #pragma unroll
@@ -99,6 +98,12 @@ __global__ __launch_bounds__(512) void delta_grads_kernel(DeltaArgs a) {
       xs[i] = buf_load16(rs, off, (pb * SE + i * NTH) * 16);
       xd[i] = buf_load16(rd, off, (pb * SE + i * NTH) * 16);
     }
+  };
+  auto load = [&](int hh, int pb) {
+    const int h = grp * per + hh;
+    const int64_t kh = (int64_t)ck * a.H + h;
+    int td = tid;  // (not seen to be the same: the offsets are formed anew)
+    asm("" : "+v"(td));
     const brsrc rz = make_rsrc(a.Z + kh * C * P, C * P * 4), rf = make_rsrc(a.F + kh * C * P, C * P * 4);
 #pragma unroll
     for (int i = 0; i < RC; ++i) {
@@ -141,6 +146,7 @@ __global__ __launch_bounds__(512) void delta_grads_kernel(DeltaArgs a) {
     }
   };
 
+  load_s(0, 0);
   load(0, 0);
 #pragma unroll 1
   for (int hh = 0; hh < per; ++hh) {
@@ -249,6 +255,10 @@ __global__ __launch_bounds__(512) void delta_grads_kernel(DeltaArgs a) {
               cc[J] = mma<PM>(jf, lds_cols<PM>(Xl + 32 * ks * LC + 16 * tb, LC, UPL, ln), cc[J]);
           }
       }
+      if constexpr (NB > 1) {
+        const int it = min(hh * NB + pb + 1, per * NB - 1);
+        load_s(it / NB, it % NB);
+      }
       __syncthreads();
     }
 #pragma unroll
@@ -347,6 +357,8 @@ __global__ __launch_bounds__(512) void delta_grads_kernel(DeltaArgs a) {
         }
         __builtin_amdgcn_sched_barrier(0);
       }
+    if constexpr (NB == 1) load_s(min(hh + 1, per - 1), 0);
+    __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
     for (int b = 0; b < 2; ++b) {
       const int tok = 16 * (2 * tp + b) + r2;
