@@ -444,8 +444,9 @@ ssd_status ssd_gated_rmsnorm_bwd(const ssd_norm_problem* problem, const void* do
  *  - Tokens behind the last sequence of cu_seqlens are not computed: their rows of
  *    every output stay as they were.
  *  - Supported: io dtype f32 or bf16; headdim and dstate in {16, 32, 64, 128};
- *    nheads % ngroups == 0; 64 * nheads * headdim * 4 and 64 * ngroups * dstate * 4 at
- *    most 2^31 - 1; finite scale; any seqlen >= 0.
+ *    nheads % ngroups == 0; nheads and nseq at most 65535; batch * seqlen < 2^30; finite
+ *    scale; any seqlen >= 0; fewer than 2^23 pairs of chunk and head, and of state and 16
+ *    of its rows.
  *  - flags: SSD_FLAG_SAVE_FOR_BWD (ssd_delta_fwd) and SSD_FLAG_FROM_SAVED
  *    (ssd_delta_bwd), with the meaning they have for ssd_fwd and ssd_bwd; any other bit
  *    is SSD_ERR_UNSUPPORTED.

@@ -37,10 +37,7 @@ ssd_status make_delta(const ssd_delta_problem* pr, int packed, DeltaProb& p) {
   if (!std::isfinite(pr->scale)) return SSD_ERR_UNSUPPORTED;
   const int64_t tokens = (int64_t)pr->batch * pr->seqlen;
   if (tokens > INT32_MAX / 2 || pr->nheads > 65535) return SSD_ERR_UNSUPPORTED;
-  // a chunk's token rows are addressed with 32-bit byte offsets
-  if ((int64_t)kDeltaChunk * pr->nheads * pr->headdim * 4 > INT32_MAX ||
-      (int64_t)kDeltaChunk * pr->ngroups * pr->dstate * 4 > INT32_MAX)
-    return SSD_ERR_UNSUPPORTED;
+  // (so that 32-bit byte offsets reach the token rows of a chunk: 64 x 65535 x 128 x 4 < 2^31)
   std::memset(&p, 0, sizeof(p));
   p.B = pr->batch;
   p.L = pr->seqlen;
@@ -56,9 +53,9 @@ ssd_status make_delta(const ssd_delta_problem* pr, int packed, DeltaProb& p) {
   if (packed && p.nst > 65535) return SSD_ERR_UNSUPPORTED;
   const int Q = kDeltaChunk;
   p.nck = packed ? ((int64_t)p.L + (int64_t)p.nst * (Q - 1)) / Q : (int64_t)p.B * ((p.L + Q - 1) / Q);
-  // 1-D grids over (chunk, head) and (state, head, 16 columns) stay below 2^31 workgroups
-  if (p.nck * (int64_t)p.H > INT32_MAX / 16 || (int64_t)p.nst * p.H * (p.P / 16) > INT32_MAX / 16)
-    return SSD_ERR_UNSUPPORTED;
+  // 1-D grids over (chunk, head) and (state, head, 16 rows) of up to 512 threads stay below
+  // the 2^32 threads of a launch
+  if (p.nck * (int64_t)p.H >= 1 << 23 || (int64_t)p.nst * p.H * (p.P / 16) >= 1 << 23) return SSD_ERR_UNSUPPORTED;
   p.map.Q = Q;
   p.map.nck = (int32_t)p.nck;
   p.map.packed = packed;
