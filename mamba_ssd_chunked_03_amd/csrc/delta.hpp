@@ -30,6 +30,17 @@ constexpr int kDeltaChunk = 64;
 // Natural-log gates below this are taken as this: exp of it is zero in fp32, and
 // running sums of it stay finite (a gate of -inf resets the state).
 constexpr float kDeltaMinGate = -256.f;
+// (a NaN stays one)
+__device__ __forceinline__ float min_gate(float g) { return g < kDeltaMinGate ? kDeltaMinGate : g; }
+
+// Whether sequence b of a call on slots runs (asked by a whole workgroup of 256): its slot lies in
+// [0, nslots) and no earlier sequence names it.  mine = slots[min(threadIdx.x, b)], loaded by
+// the caller beside its data.
+__device__ __forceinline__ bool slot_runs(const int32_t* slots, int b, int slot, int nslots, int32_t mine) {
+  int dup = (int)threadIdx.x < b && mine == slot;
+  for (int i = threadIdx.x + 256; i < b; i += 256) dup |= slots[i] == slot;
+  return !__syncthreads_or(dup) && slot >= 0 && slot < nslots;
+}
 
 struct DeltaProb {
   int32_t B, L, H, P, N, G;

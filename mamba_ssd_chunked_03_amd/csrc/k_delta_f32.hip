@@ -106,7 +106,7 @@ __global__ __launch_bounds__(256) void delta_f32_prep_kernel(DeltaArgs a, int hs
 
   // gates: lane = token; past the chunk's end the decay stays and beta is zero
   const int64_t tok = (int64_t)ci.start + lane;
-  const float gv = lane < ci.len ? fmaxf(a.g[tok * a.H + h], kDeltaMinGate) : 0.f;
+  const float gv = lane < ci.len ? min_gate(a.g[tok * a.H + h]) : 0.f;
   const float bv = lane < ci.len ? a.beta[tok * a.H + h] : 0.f;
   double G = (double)gv * 1.4426950408889634073599;
 #pragma unroll

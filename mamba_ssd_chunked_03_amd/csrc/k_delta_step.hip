@@ -7,7 +7,9 @@
 // takes some rows of one (sequence, head), N / 4 lanes a row with 4 elements each, and
 // holds them in registers over the T tokens.
 //
-// Bound: the states' bytes, read once and written once (8 bytes an element).
+// Bound: the states' bytes, read once and written once (8 bytes an element), past the caches
+// (250 sequences of 64 heads of 64 x 128, 1.05 GB: 176 us, 5.95 TB/s; 183 us with plain loads and
+// stores; 5.95 TB/s is also what a copy in place reaches).  One sequence: 3.8 us, latency.
 //
 // A sequence whose slot is out of range is padding: nothing of it is read or written.
 // Of several sequences that name one slot the first runs and the others are treated
@@ -46,13 +48,6 @@ __device__ __forceinline__ float dot4(f32x4 a, f32x4 b) {
   return a[0] * b[0] + a[1] * b[1] + a[2] * b[2] + a[3] * b[3];
 }
 
-// Whether sequence b runs: its slot lies in [0, nslots) and no earlier sequence names it.
-__device__ __forceinline__ bool slot_runs(const int32_t* slots, int b, int slot, int nslots) {
-  int dup = 0;
-  for (int i = threadIdx.x; i < b; i += blockDim.x) dup |= slots[i] == slot;
-  return !__syncthreads_or(dup) && slot >= 0 && slot < nslots;
-}
-
 template <int N, class IO, int RPT>
 __global__ __launch_bounds__(256) void delta_step_kernel(int T, int H, int G, int P, float scale,
                                                          const typename IO::T* __restrict__ Q,
@@ -66,46 +61,73 @@ __global__ __launch_bounds__(256) void delta_step_kernel(int T, int H, int G, in
   const int rb = blockIdx.x % blocks, h = (int)((blockIdx.x / blocks) % H), b = (int)(blockIdx.x / blocks / H);
   const int lr = threadIdx.x / LPR, n0 = (threadIdx.x % LPR) * 4;
   const int slot = slots ? slots[b] : b;
-  if (slots) {
-    if (!slot_runs(slots, b, slot, nslots)) return;  // (the same for the whole workgroup)
-  }
-  float* S = states + ((int64_t)slot * H + h) * P * N;
-  f32x4 s[RPT];
+  // a token's inputs, loaded while the one before is worked on (the first: beside the slots; the
+  // state after them: before the slots' check it costs 10%, its reads then run ahead of the writes)
+  const int grp = h / (H / G);
+  f32x4 k, q;
+  float gt, bt, v[RPT];
   int p[RPT];
 #pragma unroll
-  for (int i = 0; i < RPT; ++i) {
-    p[i] = rb * RP * RPT + i * RP + lr;
-    s[i] = p[i] < P ? *(const f32x4*)(S + (int64_t)p[i] * N + n0) : f32x4{0.f, 0.f, 0.f, 0.f};
-  }
-  const int grp = h / (H / G);
+  for (int i = 0; i < RPT; ++i) p[i] = rb * RP * RPT + i * RP + lr;
+  auto load = [&](int t) {
+    const int64_t tok = (int64_t)b * T + t;
+    k = io4(K + (tok * G + grp) * N + n0);
+    q = io4(Q + (tok * G + grp) * N + n0);
+    gt = g[tok * H + h];
+    bt = beta[tok * H + h];
+#pragma unroll
+    for (int i = 0; i < RPT; ++i) v[i] = io1(V + (tok * H + h) * P + min(p[i], P - 1));
+  };
+  const int32_t mine = slots ? slots[min((int)threadIdx.x, b)] : 0;
+  load(0);
+  if (slots && !slot_runs(slots, b, slot, nslots, mine)) return;  // (the same for the whole workgroup)
+  float* S = states + ((int64_t)slot * H + h) * P * N;
+  f32x4 s[RPT];
+#pragma unroll
+  for (int i = 0; i < RPT; ++i)
+    s[i] = p[i] < P ? __builtin_nontemporal_load((const f32x4*)(S + (int64_t)p[i] * N + n0)) : f32x4{0.f, 0.f, 0.f, 0.f};
   for (int t = 0; t < T; ++t) {
     const int64_t tok = (int64_t)b * T + t;
-    const f32x4 k = io4(K + (tok * G + grp) * N + n0), q = io4(Q + (tok * G + grp) * N + n0);
-    const float a = expf(fmaxf(g[tok * H + h], kDeltaMinGate)), bt = beta[tok * H + h];
-    const float kq = row_total<LPR>(dot4(k, q));
+    const f32x4 kt = k, qt = q;
+    const float a = expf(min_gate(gt)), b1 = bt;
+    float vt[RPT];
+#pragma unroll
+    for (int i = 0; i < RPT; ++i) vt[i] = v[i];
+    if (t + 1 < T) load(t + 1);
+    const float kq = row_total<LPR>(dot4(kt, qt));
 #pragma unroll
     for (int i = 0; i < RPT; ++i) {
-      const float v = p[i] < P ? io1(V + (tok * H + h) * P + p[i]) : 0.f;
-      const float sk = row_total<LPR>(dot4(s[i], k)), sq = row_total<LPR>(dot4(s[i], q));
-      const float u = bt * (v - a * sk);
+      const float sk = row_total<LPR>(dot4(s[i], kt)), sq = row_total<LPR>(dot4(s[i], qt));
+      const float u = b1 * (vt[i] - a * sk);
 #pragma unroll
-      for (int e = 0; e < 4; ++e) s[i][e] = a * s[i][e] + u * k[e];
+      for (int e = 0; e < 4; ++e) s[i][e] = a * s[i][e] + u * kt[e];
       if (n0 == 0 && p[i] < P) put1(out + (tok * H + h) * P + p[i], scale * (a * sq + u * kq));
     }
   }
 #pragma unroll
   for (int i = 0; i < RPT; ++i)
-    if (p[i] < P) *(f32x4*)(S + (int64_t)p[i] * N + n0) = s[i];
+    if (p[i] < P) __builtin_nontemporal_store(s[i], (f32x4*)(S + (int64_t)p[i] * N + n0));
 }
 
 template <int N, class IO>
 static void step_go(const DeltaProb& p, const void* q, const void* k, const void* v, const float* g,
                     const float* beta, const int32_t* slots, int nslots, float* states, void* out, hipStream_t st) {
-  constexpr int RPT = 2, RP = 256 / (N / 4);
-  const int64_t wgs = (int64_t)p.B * p.H * ((p.P + RP * RPT - 1) / (RP * RPT));
   using T = typename IO::T;
-  hipLaunchKernelGGL((delta_step_kernel<N, IO, RPT>), dim3((unsigned)wgs), dim3(256), 0, st, p.L, p.H, p.G, p.P,
-                     p.scale, (const T*)q, (const T*)k, (const T*)v, g, beta, slots, nslots, states, (T*)out);
+  constexpr int RP = 256 / (N / 4);
+  auto go = [&](auto rpt, int64_t wgs) {
+    hipLaunchKernelGGL((delta_step_kernel<N, IO, decltype(rpt)::value>), dim3((unsigned)wgs), dim3(256), 0, st, p.L, p.H,
+                       p.G, p.P, p.scale, (const T*)q, (const T*)k, (const T*)v, g, beta, slots, nslots, states,
+                       (T*)out);
+  };
+  auto count = [&](int rpt) { return (int64_t)p.B * p.H * ((p.P + RP * rpt - 1) / (RP * rpt)); };
+  // Rows a thread.  Several tokens: four, which share a token's loads, k . q and gate (5 tokens,
+  // 24 sequences of 32 heads of 128 x 128: 32 us, two rows 36), unless they leave CUs without
+  // work.  One token: two (250 sequences of 64 heads of 64 x 128: one row 289 us, two 188,
+  // four 202, eight 199; one sequence: 3.7, 3.9, 5.3, 5.6).
+  if (p.L > 1 && count(4) >= 1024)
+    go(std::integral_constant<int, 4>{}, count(4));
+  else
+    go(std::integral_constant<int, 2>{}, count(2));
 }
 
 hipError_t launch_delta_step(const DeltaProb& p, const void* q, const void* k, const void* v, const float* g,

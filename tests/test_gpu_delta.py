@@ -295,3 +295,32 @@ def test_library_status_reaches_the_caller():
     assert e.value.status == 5  # the workspace is too small
     p = ssd.DeltaProblem(1, 10, 2, 16, 16, 1, 0, 1, 0, 1.0)
     assert ssd.lib().ssd_delta_fwd_workspace_bytes(ctypes.byref(p), 0) > 16
+
+
+@pytest.mark.parametrize("io,dims", [("bf16", (4, 2, 64, 128)), ("f32", (4, 2, 32, 64))])
+def test_a_nan_gate_is_not_dropped(io, dims):
+    """The head's outputs are NaN from that token on, its final state is; the other heads and
+    sequences are those of the same call without it, bit for bit."""
+    H, G, P, N = dims
+    d = make(1, 300, H, G, P, N, io=io, lengths=[130, 170], seed=5)
+    c = cuda(d)
+    ref, rfin = run_fwd(d)
+    g = c["g"].clone()
+    g[0, 70, 1] = float("nan")
+    out, fin = ssd.delta_fwd(c["q"], c["k"], c["v"], g, c["beta"], scale=d["scale"], init=c["init"],
+                             cu_seqlens=c["cu"])
+    assert torch.isnan(out[0, 70:130, 1].float()).all() and torch.isnan(fin[0, 1]).all()
+    assert torch.equal(out[0, :64], ref[0, :64])  # the chunks before
+    keep = [0, 2, 3]
+    assert torch.equal(out[:, :, keep], ref[:, :, keep]) and torch.equal(fin[:, keep], rfin[:, keep])
+    assert torch.equal(out[:, 130:], ref[:, 130:]) and torch.equal(fin[1], rfin[1])
+    s0 = torch.ones(2, H, P, N, device="cuda")
+    s1, step = s0.clone(), (c["q"][:, :2].transpose(0, 1).contiguous(), c["k"][:, :2].transpose(0, 1).contiguous(),
+                            c["v"][:, :2].transpose(0, 1).contiguous())
+    gs = torch.zeros(2, 1, H, device="cuda")
+    o0 = ssd.delta_step(*step, gs, gs + 0.5, s0)
+    gs[1, 0, 2] = float("nan")
+    o1 = ssd.delta_step(*step, gs, torch.full_like(gs, 0.5), s1)
+    assert torch.isnan(o1[1, 0, 2].float()).all() and torch.isnan(s1[1, 2]).all()
+    o1[1, 0, 2], s1[1, 2] = o0[1, 0, 2], s0[1, 2]
+    assert torch.equal(o0, o1) and torch.equal(s0, s1)
