@@ -69,6 +69,14 @@ __device__ __forceinline__ void interleave() {
   }
 }
 
+// Chain waves a tile of 16 columns of headdim: the 128 columns of the state are dealt to two.
+template <int N>
+constexpr int kSplit = N == 128 ? 2 : 1;
+
+constexpr int kNumCu = 256;
+// Tiles a workgroup of a chain: two where one each would not fit the CUs at once.
+inline bool two_tiles(int64_t heads, int ptiles) { return ptiles >= 2 && heads * ptiles > kNumCu; }
+
 // (sequence, workgroup of the sequence) of a chain's workgroup: each XCD takes the same part
 // of every sequence's `per` workgroups (heads of one group share K and Q in its L2), so that
 // a long sequence among short ones is spread over all of them.

@@ -11,18 +11,22 @@
 //   interval A(c)  chain: K dS^T, E                 helpers: T(c), Q, P, dO(c - 1) to LDS
 //   interval B(c)  chain: (b R)^T E, F, the new dS   helpers: K, R(c - 1) to LDS, E0, T of c - 1
 // Two planes throughout (the error of dS is not a result: 3e-6 of the gradients).
+// 2 x 8192 tokens of 64 heads of 64 x 128: 380 us (one wave a tile, four tiles: 440), of
+// which dS and F written (805 MB) are 160 at the rate of a large copy.
 #include "delta_reg.hpp"
 
 namespace ssd {
 
 template <int N, int NPT>
-__global__ __launch_bounds__(64 * NPT + 256, 1) void delta_bwd_kernel(DeltaArgs a, int ptiles) {
-  constexpr int C = kDeltaChunk, NP = N < 32 ? 32 : N, KS = NP / 32;
+__global__ __launch_bounds__(64 * NPT * kSplit<N> + 256, 1) void delta_bwd_kernel(DeltaArgs a, int ptiles) {
+  constexpr int C = kDeltaChunk, NP = N < 32 ? 32 : N, KS = NP / 32, SPLIT = kSplit<N>, CW = NPT * SPLIT;
+  constexpr int KH = KS / SPLIT;  // blocks of 32 columns of the state a chain wave holds
   using Tile = TokTile<NP>;
   constexpr int LV = 16 * NPT + 8, EV = C * LV, ER = 2 * kTriPlane;
   __shared__ __align__(16) uint16_t Kl[2][Tile::SIZE], Ql[Tile::SIZE], Rl[2][ER], Pl[ER], Ol[EV];
   __shared__ __align__(16) float gl[2][3 * C];  // exp(G), exp(G_C - G), beta exp(G)
   __shared__ __align__(16) f32x4 Ex[NPT][4][64], Tx[NPT][KS][2][64];  // E0 and T, tile order
+  __shared__ __align__(16) f32x4 Kx[SPLIT == 2 ? NPT : 1][SPLIT][4][64];  // parts of K dS^T
 
   const int tid = threadIdx.x, w = __builtin_amdgcn_readfirstlane(tid >> 6), lane = tid & 63, q = lane >> 4, r = lane & 15;
   const int np = (ptiles + NPT - 1) / NPT;
@@ -36,15 +40,16 @@ __global__ __launch_bounds__(64 * NPT + 256, 1) void delta_bwd_kernel(DeltaArgs 
   const int c0 = sp.c0, c1 = sp.c1;
   const f32x4 zero = {0.f, 0.f, 0.f, 0.f};
 
-  if (w < NPT) {
+  if (w < CW) {
     // ------------------------------------------------------------ chain wave ----
-    const bool live = 16 * w < pw;
-    const int pc = p0 + 16 * w + r;
-    f32x4 S[KS][2];
+    const int tw = w / SPLIT, half = w % SPLIT, kb = half * KH;
+    const bool live = 16 * tw < pw;
+    const int pc = p0 + 16 * tw + r;
+    f32x4 S[KH][2];  // columns 32(kb + k) + 8q + 4t + e of row pc
     const int64_t srow = (((int64_t)s * a.H + h) * a.P + pc) * N;
-    auto scol = [&](int k, int t) { return 32 * k + 8 * q + 4 * t; };
+    auto scol = [&](int k, int t) { return 32 * (kb + k) + 8 * q + 4 * t; };
 #pragma unroll
-    for (int k = 0; k < KS; ++k)
+    for (int k = 0; k < KH; ++k)
 #pragma unroll
       for (int t = 0; t < 2; ++t)
         S[k][t] = a.d_final && live && scol(k, t) < N ? *(const f32x4*)(a.d_final + srow + scol(k, t)) : zero;
@@ -52,131 +57,250 @@ __global__ __launch_bounds__(64 * NPT + 256, 1) void delta_bwd_kernel(DeltaArgs 
     f32x4* kF = (f32x4*)a.F + (int64_t)(pc >> 4) * 4 * 64 + lane;
     __syncthreads();
     __syncthreads();
-    for (int c = c1 - 1; c >= c0; --c) {
-      const uint16_t* K = Kl[(c1 - 1 - c) & 1];
-      const float* g = gl[(c1 - 1 - c) & 1];
-      const int64_t kh = (int64_t)c * a.H + h;
-      // interval A: E, tile i = 2B + t with tokens 32B + 8q + 4t + e; block 1 of the tokens with
-      // dS's planes on the way, block 0 with E of block 1
-      f32x4 ks[4], E[4], er[4], wg4[4];
-      Planes<2> ef[2], Rf[6];
-      bf16x8 kt[KS][2][2];  // K^T, by block of tokens
-      const float eC = g[C - 1];
-      bf16x8 kf[KS][2], kg[KS][2];
-      Planes<2> sf[KS];
+    if constexpr (SPLIT == 2) {
+      for (int c = c1 - 1; c >= c0; --c) {
+        const uint16_t* K = Kl[(c1 - 1 - c) & 1];
+        const float* g = gl[(c1 - 1 - c) & 1];
+        const int64_t kh = (int64_t)c * a.H + h;
+        // interval A: this half's part of K dS^T
+        f32x4 ks[4], E[4], er[4], wg4[4];
+        Planes<2> ef[2], Rf[6], sf[KH];
+        bf16x8 kt[KH][2][2], kf[KH][4];
+        const float eC = g[C - 1];
 #pragma unroll
-      for (int k = 0; k < KS; ++k)
+        for (int k = 0; k < KH; ++k)
 #pragma unroll
-        for (int t = 0; t < 2; ++t) kf[k][t] = tok_rows<NP>(K, 32, t, 32 * k, lane);
+          for (int i = 0; i < 4; ++i) kf[k][i] = tok_rows<NP>(K, 32 * (i >> 1), i & 1, 32 * (kb + k), lane);
+        sf[0] = tile_planes<2>(S[0][0], S[0][1]);
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        ks[i] = zero;
-        E[i] = Ex[w][i][lane];
-        er[i] = *(const f32x4*)(g + C + 32 * (i >> 1) + 8 * q + 4 * (i & 1));
-        wg4[i] = *(const f32x4*)(g + 2 * C + 32 * (i >> 1) + 8 * q + 4 * (i & 1));
-      }
-#pragma unroll
-      for (int k = 0; k < KS; ++k)
-#pragma unroll
-        for (int t = 0; t < 2; ++t) kg[k][t] = tok_rows<NP>(K, 0, t, 32 * k, lane);
-      sf[0] = tile_planes<2>(S[0][0], S[0][1]);
-      __builtin_amdgcn_sched_barrier(0);
-#pragma unroll
-      for (int k = 0; k < KS; ++k) {
-#pragma unroll
-        for (int m = 1; m >= 0; --m)
-#pragma unroll
-          for (int t = 0; t < 2; ++t) ks[2 + t] = mfma_bf16(kf[k][t], sf[k].p[m], ks[2 + t]);
-        if (k + 1 < KS) sf[k + 1] = tile_planes<2>(S[k + 1][0], S[k + 1][1]);
-        if (live)
-#pragma unroll
-          for (int t = 0; t < 2; ++t) kS[(kh * (a.P / 16) * (KS * 2) + k * 2 + t) * 64] = S[k][t];
-        interleave<4, 4>();
+        for (int i = 0; i < 4; ++i) {
+          ks[i] = zero;
+          E[i] = Ex[tw][i][lane];
+        }
         __builtin_amdgcn_sched_barrier(0);
-      }
-      auto form_e = [&](int B) {
 #pragma unroll
-        for (int i = 2 * B; i < 2 * B + 2; ++i) E[i] += er[i] * ks[i];
-        ef[B] = tile_planes<2>(E[2 * B], E[2 * B + 1]);
-      };
-      // (and what the next interval starts with)
+        for (int k = 0; k < KH; ++k) {
 #pragma unroll
-      for (int i = 0; i < 6; ++i)
+          for (int m = 1; m >= 0; --m)
 #pragma unroll
-        for (int m = 0; m < 2; ++m)
-          Rf[i].p[m] = as_bf16x8(*(const u32x4*)(Rl[(c1 - 1 - c) & 1] + m * kTriPlane + i * 512 + lane * 8));
+            for (int i = 0; i < 4; ++i) ks[i] = mfma_bf16(kf[k][i], sf[k].p[m], ks[i]);
+          if (k + 1 < KH) sf[k + 1] = tile_planes<2>(S[k + 1][0], S[k + 1][1]);
+          if (live)
 #pragma unroll
-      for (int k = 0; k < KS; ++k)
+            for (int t = 0; t < 2; ++t) kS[(kh * (a.P / 16) * (KS * 2) + (kb + k) * 2 + t) * 64] = S[k][t];
+          if (k + 1 == KH) {
 #pragma unroll
-        for (int t = 0; t < 2; ++t) kt[k][t][1] = tok_cols<NP>(K, 32, t, 32 * k, lane);
-      __builtin_amdgcn_sched_barrier(0);
+            for (int i = 0; i < 4; ++i) {
+              er[i] = *(const f32x4*)(g + C + 32 * (i >> 1) + 8 * q + 4 * (i & 1));
+              wg4[i] = *(const f32x4*)(g + 2 * C + 32 * (i >> 1) + 8 * q + 4 * (i & 1));
+            }
 #pragma unroll
-      for (int k = 0; k < KS; ++k)
+            for (int i = 0; i < 6; ++i)
 #pragma unroll
-        for (int m = 1; m >= 0; --m)
+              for (int m = 0; m < 2; ++m)
+                Rf[i].p[m] = as_bf16x8(*(const u32x4*)(Rl[(c1 - 1 - c) & 1] + m * kTriPlane + i * 512 + lane * 8));
+          }
+          interleave<8, 3>();
+          __builtin_amdgcn_sched_barrier(0);
+        }
 #pragma unroll
-          for (int t = 0; t < 2; ++t) ks[t] = mfma_bf16(kg[k][t], sf[k].p[m], ks[t]);
-      form_e(1);
-      interleave<4 * KS, 3>();
-      __builtin_amdgcn_sched_barrier(0);
-      form_e(0);
-      __syncthreads();
-      // interval B: F = E - (b R)^T E, by planes, with dS's decay on the way
-      f32x4 F[4];
+        for (int i = 0; i < 4; ++i) Kx[tw][half][i][lane] = ks[i];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) F[i] = zero;
+        for (int k = 0; k < KH; ++k)
 #pragma unroll
-      for (int k = 0; k < KS; ++k)
+          for (int t = 0; t < 2; ++t)
 #pragma unroll
-        for (int t = 0; t < 2; ++t) kt[k][t][0] = tok_cols<NP>(K, 0, t, 32 * k, lane);
-      __builtin_amdgcn_sched_barrier(0);
+            for (int B = 0; B < 2; ++B) kt[k][t][B] = tok_cols<NP>(K, 32 * B, t, 32 * (kb + k), lane);
 #pragma unroll
-      for (int m = 0; m < 3; ++m)
+        for (int i = 0; i < 4; ++i) E[i] += er[i] * ks[i];
+        __syncthreads();
+        // interval B: E from both parts and F (each wave forms all of them, to the order of one
+        // sum), and this half of the new dS
+        f32x4 F[4], kx[4];
 #pragma unroll
-        for (int t = 0; t < 2; ++t) F[2 + t] = mfma_bf16(Rf[up_block(1, t, 1)].p[m == 0], ef[1].p[m == 1], F[2 + t]);
+        for (int i = 3; i >= 0; --i) kx[i] = Kx[tw][1 - half][i][lane];
+        __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-      for (int B2 = 1; B2 >= 0; --B2)
+        for (int i = 0; i < 4; ++i) F[i] = zero;
+#pragma unroll
+        for (int i = 2; i < 4; ++i) E[i] += er[i] * kx[i];
+        ef[1] = tile_planes<2>(E[2], E[3]);
+        __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+        for (int m = 0; m < 3; ++m) {
+#pragma unroll
+          for (int t = 0; t < 2; ++t) F[2 + t] = mfma_bf16(Rf[up_block(1, t, 1)].p[m == 0], ef[1].p[m == 1], F[2 + t]);
+#pragma unroll
+          for (int t = 0; t < 2; ++t) F[t] = mfma_bf16(Rf[up_block(0, t, 1)].p[m == 0], ef[1].p[m == 1], F[t]);
+        }
+#pragma unroll
+        for (int i = 0; i < 2; ++i) E[i] += er[i] * kx[i];
+        ef[0] = tile_planes<2>(E[0], E[1]);
+        interleave<12, 3>();
+        __builtin_amdgcn_sched_barrier(0);
+        Planes<2> wf[2];
+        auto form_w = [&](int B) {
+          f32x4 wv[2];
+#pragma unroll
+          for (int t = 0; t < 2; ++t) {
+            const int i = 2 * B + t;
+            F[i] = E[i] - F[i];
+            if (live && B == half) kF[(kh * (a.P / 16) * 4 + i) * 64] = F[i];
+            wv[t] = -(wg4[i] * F[i]);
+          }
+          wf[B] = tile_planes<2>(wv[0], wv[1]);
+        };
 #pragma unroll
         for (int m = 0; m < 3; ++m)
 #pragma unroll
-          for (int t = 0; t < 2; ++t) F[t] = mfma_bf16(Rf[up_block(0, t, B2)].p[m == 0], ef[B2].p[m == 1], F[t]);
+          for (int t = 0; t < 2; ++t) F[t] = mfma_bf16(Rf[up_block(0, t, 0)].p[m == 0], ef[0].p[m == 1], F[t]);
 #pragma unroll
-      for (int k = 0; k < KS; ++k)
+        for (int k = 0; k < KH; ++k)
 #pragma unroll
-        for (int t = 0; t < 2; ++t) S[k][t] = eC * S[k][t] + Tx[w][k][t][lane];
-      interleave<18, 2>();
-      __builtin_amdgcn_sched_barrier(0);
-      Planes<2> wf[2];
-      auto form_w = [&](int B) {
-        f32x4 wv[2];
-#pragma unroll
-        for (int t = 0; t < 2; ++t) {
-          const int i = 2 * B + t;
-          F[i] = E[i] - F[i];
-          if (live) kF[(kh * (a.P / 16) * 4 + i) * 64] = F[i];
-          wv[t] = -(wg4[i] * F[i]);
-        }
-        wf[B] = tile_planes<2>(wv[0], wv[1]);
-      };
-      form_w(1);
-      __builtin_amdgcn_sched_barrier(0);
-#pragma unroll
-      for (int B = 1; B >= 0; --B) {
-#pragma unroll
-        for (int m = 1; m >= 0; --m)
-#pragma unroll
-          for (int k = 0; k < KS; ++k)
-#pragma unroll
-            for (int t = 0; t < 2; ++t) S[k][t] = mfma_bf16(kt[k][t][B], wf[B].p[m], S[k][t]);
-        if (B == 1) form_w(0);
-        interleave<4 * KS, 2>();
+          for (int t = 0; t < 2; ++t) S[k][t] = eC * S[k][t] + Tx[tw][kb + k][t][lane];
+        form_w(1);
         __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+        for (int B = 1; B >= 0; --B) {
+#pragma unroll
+          for (int m = 1; m >= 0; --m)
+#pragma unroll
+            for (int k = 0; k < KH; ++k)
+#pragma unroll
+              for (int t = 0; t < 2; ++t) S[k][t] = mfma_bf16(kt[k][t][B], wf[B].p[m], S[k][t]);
+          if (B == 1) form_w(0);
+          interleave<4 * KH, 4>();
+          __builtin_amdgcn_sched_barrier(0);
+        }
+        __syncthreads();
       }
-      __syncthreads();
+    } else {
+      for (int c = c1 - 1; c >= c0; --c) {
+        const uint16_t* K = Kl[(c1 - 1 - c) & 1];
+        const float* g = gl[(c1 - 1 - c) & 1];
+        const int64_t kh = (int64_t)c * a.H + h;
+        // interval A: E, tile i = 2B + t with tokens 32B + 8q + 4t + e; block 1 of the tokens with
+        // dS's planes on the way, block 0 with E of block 1
+        f32x4 ks[4], E[4], er[4], wg4[4];
+        Planes<2> ef[2], Rf[6];
+        bf16x8 kt[KS][2][2];  // K^T, by block of tokens
+        const float eC = g[C - 1];
+        bf16x8 kf[KS][2], kg[KS][2];
+        Planes<2> sf[KS];
+#pragma unroll
+        for (int k = 0; k < KS; ++k)
+#pragma unroll
+          for (int t = 0; t < 2; ++t) kf[k][t] = tok_rows<NP>(K, 32, t, 32 * k, lane);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          ks[i] = zero;
+          E[i] = Ex[w][i][lane];
+          er[i] = *(const f32x4*)(g + C + 32 * (i >> 1) + 8 * q + 4 * (i & 1));
+          wg4[i] = *(const f32x4*)(g + 2 * C + 32 * (i >> 1) + 8 * q + 4 * (i & 1));
+        }
+#pragma unroll
+        for (int k = 0; k < KS; ++k)
+#pragma unroll
+          for (int t = 0; t < 2; ++t) kg[k][t] = tok_rows<NP>(K, 0, t, 32 * k, lane);
+        sf[0] = tile_planes<2>(S[0][0], S[0][1]);
+        __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+        for (int k = 0; k < KS; ++k) {
+#pragma unroll
+          for (int m = 1; m >= 0; --m)
+#pragma unroll
+            for (int t = 0; t < 2; ++t) ks[2 + t] = mfma_bf16(kf[k][t], sf[k].p[m], ks[2 + t]);
+          if (k + 1 < KS) sf[k + 1] = tile_planes<2>(S[k + 1][0], S[k + 1][1]);
+          if (live)
+#pragma unroll
+            for (int t = 0; t < 2; ++t) kS[(kh * (a.P / 16) * (KS * 2) + k * 2 + t) * 64] = S[k][t];
+          interleave<4, 4>();
+          __builtin_amdgcn_sched_barrier(0);
+        }
+        auto form_e = [&](int B) {
+#pragma unroll
+          for (int i = 2 * B; i < 2 * B + 2; ++i) E[i] += er[i] * ks[i];
+          ef[B] = tile_planes<2>(E[2 * B], E[2 * B + 1]);
+        };
+        // (and what the next interval starts with)
+#pragma unroll
+        for (int i = 0; i < 6; ++i)
+#pragma unroll
+          for (int m = 0; m < 2; ++m)
+            Rf[i].p[m] = as_bf16x8(*(const u32x4*)(Rl[(c1 - 1 - c) & 1] + m * kTriPlane + i * 512 + lane * 8));
+#pragma unroll
+        for (int k = 0; k < KS; ++k)
+#pragma unroll
+          for (int t = 0; t < 2; ++t) kt[k][t][1] = tok_cols<NP>(K, 32, t, 32 * k, lane);
+        __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+        for (int k = 0; k < KS; ++k)
+#pragma unroll
+          for (int m = 1; m >= 0; --m)
+#pragma unroll
+            for (int t = 0; t < 2; ++t) ks[t] = mfma_bf16(kg[k][t], sf[k].p[m], ks[t]);
+        form_e(1);
+        interleave<4 * KS, 3>();
+        __builtin_amdgcn_sched_barrier(0);
+        form_e(0);
+        __syncthreads();
+        // interval B: F = E - (b R)^T E, by planes, with dS's decay on the way
+        f32x4 F[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) F[i] = zero;
+#pragma unroll
+        for (int k = 0; k < KS; ++k)
+#pragma unroll
+          for (int t = 0; t < 2; ++t) kt[k][t][0] = tok_cols<NP>(K, 0, t, 32 * k, lane);
+        __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+        for (int m = 0; m < 3; ++m)
+#pragma unroll
+          for (int t = 0; t < 2; ++t) F[2 + t] = mfma_bf16(Rf[up_block(1, t, 1)].p[m == 0], ef[1].p[m == 1], F[2 + t]);
+#pragma unroll
+        for (int B2 = 1; B2 >= 0; --B2)
+#pragma unroll
+          for (int m = 0; m < 3; ++m)
+#pragma unroll
+            for (int t = 0; t < 2; ++t) F[t] = mfma_bf16(Rf[up_block(0, t, B2)].p[m == 0], ef[B2].p[m == 1], F[t]);
+#pragma unroll
+        for (int k = 0; k < KS; ++k)
+#pragma unroll
+          for (int t = 0; t < 2; ++t) S[k][t] = eC * S[k][t] + Tx[w][k][t][lane];
+        interleave<18, 2>();
+        __builtin_amdgcn_sched_barrier(0);
+        Planes<2> wf[2];
+        auto form_w = [&](int B) {
+          f32x4 wv[2];
+#pragma unroll
+          for (int t = 0; t < 2; ++t) {
+            const int i = 2 * B + t;
+            F[i] = E[i] - F[i];
+            if (live) kF[(kh * (a.P / 16) * 4 + i) * 64] = F[i];
+            wv[t] = -(wg4[i] * F[i]);
+          }
+          wf[B] = tile_planes<2>(wv[0], wv[1]);
+        };
+        form_w(1);
+        __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+        for (int B = 1; B >= 0; --B) {
+#pragma unroll
+          for (int m = 1; m >= 0; --m)
+#pragma unroll
+            for (int k = 0; k < KS; ++k)
+#pragma unroll
+              for (int t = 0; t < 2; ++t) S[k][t] = mfma_bf16(kt[k][t][B], wf[B].p[m], S[k][t]);
+          if (B == 1) form_w(0);
+          interleave<4 * KS, 2>();
+          __builtin_amdgcn_sched_barrier(0);
+        }
+        __syncthreads();
+      }
     }
     if (a.d_init && live) {
 #pragma unroll
-      for (int k = 0; k < KS; ++k)
+      for (int k = 0; k < KH; ++k)
 #pragma unroll
         for (int t = 0; t < 2; ++t)
           if (scol(k, t) < N) *(f32x4*)(a.d_init + srow + scol(k, t)) = S[k][t];
@@ -185,8 +309,10 @@ __global__ __launch_bounds__(64 * NPT + 256, 1) void delta_bwd_kernel(DeltaArgs 
   }
 
   // --------------------------------------------------------------- helper wave ----
-  const int ht = tid - 64 * NPT, tile = w - NPT;
-  const bool works = tile < NPT && 16 * tile < pw;
+  // (of a tile: HT blocks of 16 tokens of E0 and TK blocks of 32 columns of T a wave)
+  constexpr int HT = NPT, TK = KS * NPT < 4 ? 1 : KS * NPT / 4;
+  const int ht = tid - 64 * CW, tile = (w - CW) % NPT, i0 = (w - CW) / NPT * HT, k0 = (w - CW) / NPT * TK;
+  const bool works = 16 * tile < pw, sums = works && k0 < KS;
   if constexpr (N < 32) {
     for (int e = ht; e < C; e += 256)
       for (int c = N; c < 32; c += 4) {
@@ -268,30 +394,39 @@ __global__ __launch_bounds__(64 * NPT + 256, 1) void delta_bwd_kernel(DeltaArgs 
     }
     if (ht < 3 * C) gl[buf][ht] = xg;
   };
-  f32x4 T[KS][2];
+  f32x4 T[TK][2];
   // E0 (to LDS) and T (kept) of the chunk in Pl, Ol, Ql
   auto ahead = [&](int buf) {
     if (!works) return;
     const float* g = gl[buf];
-    Planes<2> Pf[6], df[2];
+    Planes<2> Pf[HT][2], df[2];
     bf16x8 of[2];
 #pragma unroll
     for (int B = 0; B < 2; ++B) of[B] = frag_kmajor(Ol + 32 * B * LV + 16 * tile, LV, lane);
 #pragma unroll
-    for (int i = 0; i < 6; ++i)
+    for (int ii = 0; ii < HT; ++ii)
 #pragma unroll
-      for (int m = 0; m < 2; ++m) Pf[i].p[m] = as_bf16x8(*(const u32x4*)(Pl + m * kTriPlane + i * 512 + lane * 8));
-    f32x4 e0[4];
+      for (int B2 = 0; B2 < 2; ++B2) {
+        const int i = i0 + ii;
+        if (B2 || i < 2)
 #pragma unroll
-    for (int i = 0; i < 4; ++i) e0[i] = zero;
+          for (int m = 0; m < 2; ++m)
+            Pf[ii][B2].p[m] =
+                as_bf16x8(*(const u32x4*)(Pl + m * kTriPlane + up_block(i >> 1, i & 1, B2) * 512 + lane * 8));
+      }
+    f32x4 e0[HT];
+#pragma unroll
+    for (int ii = 0; ii < HT; ++ii) e0[ii] = zero;
 #pragma unroll
     for (int m = 1; m >= 0; --m)
 #pragma unroll
       for (int B2 = 1; B2 >= 0; --B2)
 #pragma unroll
-        for (int i = 0; i < (B2 ? 4 : 2); ++i) e0[i] = mfma_bf16(Pf[up_block(i >> 1, i & 1, B2)].p[m], of[B2], e0[i]);
+        for (int ii = 0; ii < HT; ++ii)
+          if (B2 || i0 + ii < 2) e0[ii] = mfma_bf16(Pf[ii][B2].p[m], of[B2], e0[ii]);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) Ex[tile][i][lane] = e0[i];
+    for (int ii = 0; ii < HT; ++ii) Ex[tile][i0 + ii][lane] = e0[ii];
+    if (!sums) return;
 #pragma unroll
     for (int B = 0; B < 2; ++B) {
       const u32x4 ow = __builtin_bit_cast(u32x4, of[B]);
@@ -303,21 +438,21 @@ __global__ __launch_bounds__(64 * NPT + 256, 1) void delta_bwd_kernel(DeltaArgs 
       df[B] = tile_planes<2>(d[0], d[1]);
     }
 #pragma unroll
-    for (int k = 0; k < KS; ++k)
+    for (int k = 0; k < TK; ++k)
 #pragma unroll
       for (int t = 0; t < 2; ++t) T[k][t] = zero;
 #pragma unroll
     for (int B = 0; B < 2; ++B) {
-      bf16x8 qf[KS][2];
+      bf16x8 qf[TK][2];
 #pragma unroll
-      for (int k = 0; k < KS; ++k)
+      for (int k = 0; k < TK; ++k)
 #pragma unroll
-        for (int t = 0; t < 2; ++t) qf[k][t] = tok_cols<NP>(Ql, 32 * B, t, 32 * k, lane);
+        for (int t = 0; t < 2; ++t) qf[k][t] = tok_cols<NP>(Ql, 32 * B, t, 32 * (k0 + k), lane);
       __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
       for (int m = 1; m >= 0; --m)
 #pragma unroll
-        for (int k = 0; k < KS; ++k)
+        for (int k = 0; k < TK; ++k)
 #pragma unroll
           for (int t = 0; t < 2; ++t) T[k][t] = mfma_bf16(qf[k][t], df[B].p[m], T[k][t]);
     }
@@ -341,11 +476,11 @@ __global__ __launch_bounds__(64 * NPT + 256, 1) void delta_bwd_kernel(DeltaArgs 
   for (int c = c1 - 1; c >= c0; --c) {
     const int nb = (c1 - c) & 1;  // the next chunk's buffer
     // interval A
-    if (works) {
+    if (sums) {
 #pragma unroll
-      for (int k = 0; k < KS; ++k)
+      for (int k = 0; k < TK; ++k)
 #pragma unroll
-        for (int t = 0; t < 2; ++t) Tx[tile][k][t][lane] = T[k][t];
+        for (int t = 0; t < 2; ++t) Tx[tile][k0 + k][t][lane] = T[k][t];
     }
     put_ahead(nb);
     load_ahead(max(c - 2, c0));
@@ -366,18 +501,12 @@ hipError_t launch_delta_bwd_chain(const DeltaProb& p, const DeltaArgs& a, hipStr
   const int ptiles = p.P / 16;
   const int64_t heads = (int64_t)p.nst * p.H;
   auto go = [&](auto n, auto npt) {
-    constexpr int NPT = decltype(npt)::value;
-    hipLaunchKernelGGL((delta_bwd_kernel<decltype(n)::value, NPT>),
-                       dim3((unsigned)(heads * ((ptiles + NPT - 1) / NPT))), dim3(64 * NPT + 256), 0, st, a, ptiles);
+    constexpr int N = decltype(n)::value, NPT = decltype(npt)::value;
+    hipLaunchKernelGGL((delta_bwd_kernel<N, NPT>), dim3((unsigned)(heads * ((ptiles + NPT - 1) / NPT))),
+                       dim3(64 * NPT * kSplit<N> + 256), 0, st, a, ptiles);
   };
   auto pick = [&](auto n) {
-    const int64_t tiles = heads * ptiles;
-    if (tiles >= 512 && ptiles >= 4)
-      go(n, std::integral_constant<int, 4>{});
-    else if (tiles >= 256 && ptiles >= 2)
-      go(n, std::integral_constant<int, 2>{});
-    else
-      go(n, std::integral_constant<int, 1>{});
+    two_tiles(heads, ptiles) ? go(n, std::integral_constant<int, 2>{}) : go(n, std::integral_constant<int, 1>{});
   };
   switch (p.N) {
     case 16: pick(std::integral_constant<int, 16>{}); break;
