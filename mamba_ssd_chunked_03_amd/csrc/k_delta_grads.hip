@@ -16,8 +16,12 @@
 // dq and dk are summed over the group's heads in registers, in order.  Eight waves: wave w
 // has tokens 32 (w % 2)..+31 and a quarter (w / 2) of the N columns, which reads each
 // operand from LDS two to four times (16 tokens and half the columns a wave: 1.3 times as
-// much); 16 rows of dP (first four waves) or dM (last four).  The running sums of a head's
-// gates are formed by one wave while the others begin the next head.
+// much; sixteen waves, 1.5 times as much, 925 us below), and three of the 24 blocks of dP and
+// dM that are formed (16 rows a wave: 5% more).  The running sums of a head's gates are formed
+// by one wave while the others begin the next head.
+// 2 x 8192 tokens, 64 heads in 8 groups, 64 x 128: 720 us, 11 a head, of which a workgroup's
+// matrix instructions take 1.7, vector ones 3.5, and LDS 5 with its conflicts: phases between
+// barriers, two waves a SIMD, with the next head's loads in flight (2.6 TB/s).
 #include "delta.hpp"
 
 namespace ssd {
@@ -25,12 +29,14 @@ namespace ssd {
 template <int N, int P, class IO>
 __global__ __launch_bounds__(512) void delta_grads_kernel(DeltaArgs a) {
   using T = typename IO::T;
-  constexpr int PI = IO::PI, PM = IO::PM, ES = sizeof(T), C = kDeltaChunk, NTH = 512;
+  constexpr int PI = IO::PI, PM = IO::PM, ES = sizeof(T), C = kDeltaChunk, NW = 8, NTH = 64 * NW;
   constexpr int NP = N < 32 ? 32 : N;
   // columns of headdim staged at a time (the products' depth is 32; past P they are zero)
   constexpr int PB = P < 32 ? 32 : (P > (PM == 2 ? 64 : 32) ? (PM == 2 ? 64 : 32) : P), NB = (P + PB - 1) / PB;
   constexpr int LN = N + 8, LP = PB + 8, LC = C + 8;  // rows: dstate; headdim; tokens
-  constexpr int TN = N / 16, TQ = (TN + 3) / 4;  // column tiles, of one quarter
+  // a wave's part of the products: TB blocks of 16 tokens, one NQ-th of the column tiles
+  constexpr int TN = N / 16, TB = 2, NT = 4 / TB, NQ = NW / NT, TQ = (TN + NQ - 1) / NQ;
+  constexpr bool FULL = TN % NQ == 0;
   constexpr int SPL = PB * LN, UPL = PB * LC, OPL = C * LP, KPL = C * LN, CPL = C * LC;
   // bf16 io: K and Q stay in LDS over the heads; fp32 io: they share the states' place
   constexpr bool KEEP = PI == 1;
@@ -39,12 +45,22 @@ __global__ __launch_bounds__(512) void delta_grads_kernel(DeltaArgs a) {
   uint16_t *Sl = lds, *Dl = Sl + PM * SPL, *Ul = Dl + PM * SPL, *Xl = Ul + PM * UPL, *Ol = Xl + PM * UPL;
   uint16_t *Pl = lds, *Ml = Pl + PM * CPL;
   uint16_t *Kl = KEEP ? lds + (PH1 > PH2 ? PH1 : PH2) : Ml + PM * CPL, *Ql = Kl + PI * KPL;
-  // gates; row dots (of G and of w) of the four quarters; parts of <S, dS> and exp(G_C); parts of dbeta
+  // gates; row dots (of G and of w) of the NQ parts; parts of <S, dS> and exp(G_C); parts of dbeta
   __shared__ __align__(16) float gl[3 * C];
-  __shared__ float red[2][4][C], sd[NTH / 64 + 1], bsum[2][C];
+  __shared__ float red[2][NQ][C], sd[NW + 1], bsum[NW / 4][C];
 
   const int tid = threadIdx.x, w = __builtin_amdgcn_readfirstlane(tid >> 6), lane = tid & 63, q = lane >> 4, r = lane & 15;
-  const int tp = w & 1, nq = w >> 1, tb = w & 3, md = w >> 2;
+  const int tp = w % NT, nq = w / NT;
+  // dP (first half of the waves) or dM, 16 x 16: ten blocks at or below the diagonal and, since a
+  // product takes 32 columns at once, zeros right of two of them; block i of a wave's
+  constexpr int CB = (12 + NW / 2 - 1) / (NW / 2);
+  const int md = w / (NW / 2);
+  auto low = [&](int i, int& t, int& j) {
+    const int b = w % (NW / 2) + i * (NW / 2);
+    t = (0x8ffa94 >> (2 * b)) & 3;
+    j = (0xde4910 >> (2 * b)) & 3;
+    return b < 12;
+  };
   const int wg = xcd_order(blockIdx.x, gridDim.x);
   const int ck = wg / a.G, grp = wg % a.G, per = a.H / a.G;
   ChunkInfo ci = chunk_info(a.map, ck);
@@ -79,9 +95,9 @@ __global__ __launch_bounds__(512) void delta_grads_kernel(DeltaArgs a) {
   // (past headdim they are zero).
   constexpr int SE = PB * NP / 4, RE = PB * C / 4, OE = C * PB / 8;
   constexpr int SC = (SE + NTH - 1) / NTH, RC = (RE + NTH - 1) / NTH, TPR = NP / 16;
-  static_assert(OE <= NTH && 3 * C <= NTH && RE % NTH == 0, "pieces of a thread");
-  // wave w's tile i of the states: rows 16 (i 8 / TPR + w / TPR).., column tile w % TPR; of Z
-  // and F: rows 16 (2i + w / 4).., token tile w % 4
+  static_assert(OE <= NTH && 3 * C <= NTH && RE % NTH == 0 && NW % TPR == 0, "pieces of a thread");
+  // wave w's tile i of the states: rows 16 (i NW / TPR + w / TPR).., column tile w % TPR; of Z
+  // and F: rows 16 (i NW / 4 + w / 4).., token tile w % 4
   const int tk4 = 32 * ((w & 3) >> 1) + 8 * q + 4 * (w & 1);  // (the same tokens in each)
   const int scol = 32 * ((w % TPR) >> 1) + 8 * q + 4 * (w & 1);
   u32x4 xs[SC], xd[SC], xz[RC], xf_[RC], xb;
@@ -119,30 +135,36 @@ __global__ __launch_bounds__(512) void delta_grads_kernel(DeltaArgs a) {
     xg = buf_load_f32(rg, td * 4);
   };
 
-  f32x4 dqs[2][TQ], dks[2][TQ];
+  f32x4 dqs[TB][TQ], dks[TB][TQ];
 #pragma unroll
-  for (int b = 0; b < 2; ++b)
+  for (int b = 0; b < TB; ++b)
 #pragma unroll
     for (int i = 0; i < TQ; ++i) dqs[b][i] = dks[b][i] = zero;
   // dg and dbeta of a head from its parts in LDS (one wave)
   auto gates = [&](int hh) {
     float t = 0.f;
 #pragma unroll
-    for (int i = 0; i < NTH / 64; ++i) t += sd[i];
+    for (int i = 0; i < NW; ++i) t += sd[i];
     // suffix sums with the tokens in reverse over the lanes, prefix sums in order
     int lane = tid & 63;
     asm("" : "+v"(lane));
     const int rl = C - 1 - lane;
-    float x = (red[0][0][rl] + red[0][1][rl]) + (red[0][2][rl] + red[0][3][rl]);
-    if (lane == 0) x += sd[NTH / 64] * t;
-    const float wj = (red[1][0][lane] + red[1][1][lane]) + (red[1][2][lane] + red[1][3][lane]);
+    float x = 0.f, wj = 0.f, db = 0.f;
+#pragma unroll
+    for (int i = 0; i < NQ; ++i) {
+      x += red[0][i][rl];
+      wj += red[1][i][lane];
+    }
+#pragma unroll
+    for (int i = 0; i < NW / 4; ++i) db += bsum[i][lane];
+    if (lane == 0) x += sd[NW] * t;
     x = wave_inclusive_sum(x);
     const float y = wave_inclusive_sum(wj) - wj;
     x = __shfl(x, rl);
     if (lane < len) {
       const int64_t at = ((int64_t)start + lane) * a.H + grp * per + hh;
       a.dg[at] = x + y;
-      a.dbeta[at] = bsum[0][lane] + bsum[1][lane];
+      a.dbeta[at] = db;
     }
   };
 
@@ -152,13 +174,13 @@ __global__ __launch_bounds__(512) void delta_grads_kernel(DeltaArgs a) {
   for (int hh = 0; hh < per; ++hh) {
     const int h = grp * per + hh;
     const brsrc rdv = make_rsrc((char*)a.dv + ((int64_t)start * a.H + h) * P * ES, (uint32_t)(len - 1) * vrow + P * ES);
-    f32x4 dq[2][TQ], dr[2][TQ], dw[2][TQ], cc[4];
+    f32x4 dq[TB][TQ], dr[TB][TQ], dw[TB][TQ], cc[CB];
 #pragma unroll
-    for (int b = 0; b < 2; ++b)
+    for (int b = 0; b < TB; ++b)
 #pragma unroll
       for (int i = 0; i < TQ; ++i) dq[b][i] = dr[b][i] = dw[b][i] = zero;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) cc[i] = zero;
+    for (int i = 0; i < CB; ++i) cc[i] = zero;
     float sdot = 0.f;
     f32x4 bdot = zero;  // F . Z of four tokens, this thread's rows
 #pragma unroll 1
@@ -168,7 +190,7 @@ __global__ __launch_bounds__(512) void delta_grads_kernel(DeltaArgs a) {
       const int lr = td & 15;
 #pragma unroll
       for (int i = 0; i < SC; ++i) {
-        const int at = (16 * (i * (8 / TPR) + w / TPR) + lr) * LN + scol;
+        const int at = (16 * (i * (NW / TPR) + w / TPR) + lr) * LN + scol;
         const f32x4 x = __builtin_bit_cast(f32x4, xs[i]), y = __builtin_bit_cast(f32x4, xd[i]);
         sdot += x[0] * y[0] + x[1] * y[1] + x[2] * y[2] + x[3] * y[3];
         if ((SE % NTH == 0 || td + i * NTH < SE) && (N == NP || scol < N)) {
@@ -184,7 +206,7 @@ __global__ __launch_bounds__(512) void delta_grads_kernel(DeltaArgs a) {
       const f32x4 b = __builtin_bit_cast(f32x4, xb);
 #pragma unroll
       for (int i = 0; i < RC; ++i) {
-        const int at = (16 * (2 * i + (w >> 2)) + lr) * LC + tk4;
+        const int at = (16 * (NW / 4 * i + (w >> 2)) + lr) * LC + tk4;
         const f32x4 z = __builtin_bit_cast(f32x4, xz[i]), f = __builtin_bit_cast(f32x4, xf_[i]);
         bdot += z * f;
         uint2 o[PM];
@@ -202,7 +224,7 @@ __global__ __launch_bounds__(512) void delta_grads_kernel(DeltaArgs a) {
         for (int m = 0; m < PI; ++m) *(u32x4*)(Ol + m * OPL + td / (PB / 8) * LP + (td % (PB / 8)) * 8) = o[m];
       }
       if (tid < 3 * C) gl[tid] = xg;
-      if (pb == 0 && hh > 0 && w == (hh & 7)) gates(hh - 1);
+      if (pb == 0 && hh > 0 && w == hh % NW) gates(hh - 1);
       if constexpr (NB > 1) {
         const int it = min(hh * NB + pb + 1, per * NB - 1);
         load(it / NB, it % NB);
@@ -214,22 +236,22 @@ __global__ __launch_bounds__(512) void delta_grads_kernel(DeltaArgs a) {
       asm("" : "+v"(ln));
 #pragma unroll 1
       for (int ks = 0; ks < PB / 32; ++ks) {
-        Planes<PI> of[2];
-        Planes<PM> xf[2], uf[2];
+        Planes<PI> of[TB];
+        Planes<PM> xf[TB], uf[TB];
 #pragma unroll
-        for (int b = 0; b < 2; ++b) {
-          of[b] = lds_rows<PI>(Ol + 16 * (2 * tp + b) * LP + 32 * ks, LP, OPL, ln);
-          xf[b] = lds_cols<PM>(Xl + 32 * ks * LC + 16 * (2 * tp + b), LC, UPL, ln);
-          uf[b] = lds_cols<PM>(Ul + 32 * ks * LC + 16 * (2 * tp + b), LC, UPL, ln);
+        for (int b = 0; b < TB; ++b) {
+          of[b] = lds_rows<PI>(Ol + 16 * (TB * tp + b) * LP + 32 * ks, LP, OPL, ln);
+          xf[b] = lds_cols<PM>(Xl + 32 * ks * LC + 16 * (TB * tp + b), LC, UPL, ln);
+          uf[b] = lds_cols<PM>(Ul + 32 * ks * LC + 16 * (TB * tp + b), LC, UPL, ln);
         }
 #pragma unroll
         for (int i = 0; i < TQ; ++i) {
           const int nt = nq * TQ + i;
-          if (TN % 4 == 0 || nt < TN) {
+          if (FULL || nt < TN) {
             const Planes<PM> sf = lds_cols<PM>(Sl + 32 * ks * LN + 16 * nt, LN, SPL, ln);
             const Planes<PM> df = lds_cols<PM>(Dl + 32 * ks * LN + 16 * nt, LN, SPL, ln);
 #pragma unroll
-            for (int b = 0; b < 2; ++b) {
+            for (int b = 0; b < TB; ++b) {
               dq[b][i] = mma<PM>(sf, of[b], dq[b][i]);
               dr[b][i] = mma<PM>(sf, xf[b], dr[b][i]);
               dw[b][i] = mma<PM>(df, uf[b], dw[b][i]);
@@ -241,19 +263,21 @@ __global__ __launch_bounds__(512) void delta_grads_kernel(DeltaArgs a) {
           const int p = pb * PB + 32 * ks + 8 * (ln >> 4);
           if (nq == 0 && p < P)
 #pragma unroll
-            for (int b = 0; b < 2; ++b)
-              buf_store16(rdv, (16 * (2 * tp + b) + (ln & 15)) * vrow + p * ES, __builtin_bit_cast(u32x4, xf[b].p[0]));
+            for (int b = 0; b < TB; ++b)
+              buf_store16(rdv, (16 * (TB * tp + b) + (ln & 15)) * vrow + p * ES, __builtin_bit_cast(u32x4, xf[b].p[0]));
         }
-        // rows j (block J) of dO U^T or dX U^T, columns i (block tb)
+        // rows j (block J) of dO U^T or dX U^T, columns i (block I)
 #pragma unroll
-        for (int J = 0; J < 4; ++J)
-          if (J <= tb) {
+        for (int i = 0; i < CB; ++i) {
+          int I, J;
+          if (low(i, I, J) && J <= I) {
             const Planes<PM> jf = lds_cols<PM>(Ul + 32 * ks * LC + 16 * J, LC, UPL, ln);
             if (md == 0)
-              cc[J] = mma<PM>(jf, lds_rows<PI>(Ol + 16 * tb * LP + 32 * ks, LP, OPL, ln), cc[J]);
+              cc[i] = mma<PM>(jf, lds_rows<PI>(Ol + 16 * I * LP + 32 * ks, LP, OPL, ln), cc[i]);
             else
-              cc[J] = mma<PM>(jf, lds_cols<PM>(Xl + 32 * ks * LC + 16 * tb, LC, UPL, ln), cc[J]);
+              cc[i] = mma<PM>(jf, lds_cols<PM>(Xl + 32 * ks * LC + 16 * I, LC, UPL, ln), cc[i]);
           }
+        }
       }
       if constexpr (NB > 1) {
         const int it = min(hh * NB + pb + 1, per * NB - 1);
@@ -262,8 +286,8 @@ __global__ __launch_bounds__(512) void delta_grads_kernel(DeltaArgs a) {
       __syncthreads();
     }
 #pragma unroll
-    for (int b = 0; b < 2; ++b) {
-      const int tok = 16 * (2 * tp + b) + r;
+    for (int b = 0; b < TB; ++b) {
+      const int tok = 16 * (TB * tp + b) + r;
       const float Gh = gl[tok], Gl = gl[C + tok];
       const float eG = exp2_hl(Gh, Gl), eR = exp2_fast((gl[C - 1] - Gh) + (gl[2 * C - 1] - Gl));
 #pragma unroll
@@ -273,30 +297,29 @@ __global__ __launch_bounds__(512) void delta_grads_kernel(DeltaArgs a) {
         dw[b][i] = eR * dw[b][i];
       }
     }
-    // dP or dM, [i][j]; the block right of an even diagonal one is read in the same step of 32
-    // and written as zero
-    {
+    // dP or dM, [i][j]
+#pragma unroll
+    for (int i = 0; i < CB; ++i) {
+      int I, J;
+      if (!low(i, I, J)) continue;
       uint16_t* dst = md == 0 ? Pl : Ml;
       const float f = md == 0 ? a.scale : -1.f;
-      const int tok = 16 * tb + r;
-      const float Gh = gl[tok], Gl = gl[C + tok];
+      const int tok = 16 * I + r;
+      f32x4 v = zero;
+      if (J <= I) {
+        const float Gh = gl[tok], Gl = gl[C + tok];
+        const f32x4 jh = *(const f32x4*)(gl + 16 * J + 4 * q), jl = *(const f32x4*)(gl + C + 16 * J + 4 * q);
 #pragma unroll
-      for (int J = 0; J < 4; ++J) {
-        if (J > tb && !(J == tb + 1 && (tb & 1) == 0)) continue;
-        f32x4 v = zero;
-        if (J <= tb) {
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const int j = 16 * J + 4 * q + e;
-            const float d = exp2_fast((Gh - gl[j]) + (Gl - gl[C + j]));
-            v[e] = (md == 0 ? j <= tok : j < tok) ? f * (cc[J][e] * d) : 0.f;
-          }
+        for (int e = 0; e < 4; ++e) {
+          const int j = 16 * J + 4 * q + e;
+          const float d = exp2_fast((Gh - jh[e]) + (Gl - jl[e]));
+          v[e] = (md == 0 ? j <= tok : j < tok) ? f * (cc[i][e] * d) : 0.f;
         }
-        uint2 o[PM];
-        split4<PM>(v, o);
-#pragma unroll
-        for (int m = 0; m < PM; ++m) *(uint2*)(dst + m * CPL + tok * LC + 16 * J + 4 * q) = o[m];
       }
+      uint2 o[PM];
+      split4<PM>(v, o);
+#pragma unroll
+      for (int m = 0; m < PM; ++m) *(uint2*)(dst + m * CPL + tok * LC + 16 * J + 4 * q) = o[m];
     }
     if constexpr (!KEEP) put_kq();
     __syncthreads();
@@ -315,14 +338,16 @@ __global__ __launch_bounds__(512) void delta_grads_kernel(DeltaArgs a) {
       }
       return v;
     };
-    float dwr[2] = {0.f, 0.f};  // this lane's part of w
+    float dwr[TB];  // this lane's part of w
     __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-    for (int b = 0; b < 2; ++b)
+    for (int b = 0; b < TB; ++b) dwr[b] = 0.f;
+#pragma unroll
+    for (int b = 0; b < TB; ++b)
 #pragma unroll
       for (int i = 0; i < TQ; ++i)
-        if (TN % 4 == 0 || nq * TQ + i < TN) {
-          const f32x4 kv = value(Kl, 16 * (2 * tp + b) + r2, nq * TQ + i);
+        if (FULL || nq * TQ + i < TN) {
+          const f32x4 kv = value(Kl, 16 * (TB * tp + b) + r2, nq * TQ + i);
 #pragma unroll
           for (int e = 0; e < 4; ++e) dwr[b] += kv[e] * dw[b][i][e];
         }
@@ -330,25 +355,25 @@ __global__ __launch_bounds__(512) void delta_grads_kernel(DeltaArgs a) {
 #pragma unroll
     for (int ks = 0; ks < 2; ++ks)
 #pragma unroll
-      for (int b = 0; b < 2; ++b) {
-        const int t0 = 16 * (2 * tp + b);
-        if (ks == 0 || tp == 1) {  // j in this block, up to i
+      for (int b = 0; b < TB; ++b) {
+        const int t0 = 16 * (TB * tp + b);
+        if (ks == 0 || TB * tp >= 2) {  // j in this block, up to i
           const Planes<PM> pr = lds_rows<PM>(Pl + t0 * LC + 32 * ks, LC, CPL, l2);
           const Planes<PM> mr = lds_rows<PM>(Ml + t0 * LC + 32 * ks, LC, CPL, l2);
 #pragma unroll
           for (int i = 0; i < TQ; ++i)
-            if (TN % 4 == 0 || nq * TQ + i < TN) {
+            if (FULL || nq * TQ + i < TN) {
               const Planes<PI> kf = lds_cols<PI>(Kl + 32 * ks * LN + 16 * (nq * TQ + i), LN, KPL, l2);
               dq[b][i] = mma<PM>(kf, pr, dq[b][i]);
               dr[b][i] = mma<PM>(kf, mr, dr[b][i]);
             }
         }
-        if (ks == 1 || tp == 0) {  // i in this block, from j on
+        if (ks == 1 || TB * tp < 2) {  // i in this block, from j on
           const Planes<PM> pc = lds_cols<PM>(Pl + 32 * ks * LC + t0, LC, CPL, l2);
           const Planes<PM> mc = lds_cols<PM>(Ml + 32 * ks * LC + t0, LC, CPL, l2);
 #pragma unroll
           for (int i = 0; i < TQ; ++i)
-            if (TN % 4 == 0 || nq * TQ + i < TN) {
+            if (FULL || nq * TQ + i < TN) {
               const Planes<PI> kf = lds_cols<PI>(Kl + 32 * ks * LN + 16 * (nq * TQ + i), LN, KPL, l2);
               const Planes<PI> qf = lds_cols<PI>(Ql + 32 * ks * LN + 16 * (nq * TQ + i), LN, KPL, l2);
               dw[b][i] = mma<PM>(qf, pc, dw[b][i]);
@@ -360,12 +385,12 @@ __global__ __launch_bounds__(512) void delta_grads_kernel(DeltaArgs a) {
     if constexpr (NB == 1) load_s(min(hh + 1, per - 1), 0);
     __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-    for (int b = 0; b < 2; ++b) {
-      const int tok = 16 * (2 * tp + b) + r2;
+    for (int b = 0; b < TB; ++b) {
+      const int tok = 16 * (TB * tp + b) + r2;
       float da = dwr[b];  // this lane's part of dL/dG
 #pragma unroll
       for (int i = 0; i < TQ; ++i)
-        if (TN % 4 == 0 || nq * TQ + i < TN) {
+        if (FULL || nq * TQ + i < TN) {
           const f32x4 kv = value(Kl, tok, nq * TQ + i), qv = value(Ql, tok, nq * TQ + i);
 #pragma unroll
           for (int e = 0; e < 4; ++e) da += qv[e] * dq[b][i][e] + kv[e] * (dr[b][i][e] - dw[b][i][e]);
@@ -383,7 +408,7 @@ __global__ __launch_bounds__(512) void delta_grads_kernel(DeltaArgs a) {
     }
     sdot = wave_sum(sdot);
     if (lane == 0) sd[w] = sdot;
-    if (tid == 0) sd[NTH / 64] = exp2_hl(gl[C - 1], gl[2 * C - 1]);
+    if (tid == 0) sd[NW] = exp2_hl(gl[C - 1], gl[2 * C - 1]);
     // F . Z over the rows: 16 lanes, then two waves in order
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
@@ -395,12 +420,12 @@ __global__ __launch_bounds__(512) void delta_grads_kernel(DeltaArgs a) {
   if (w == 0) gates(per - 1);
   const brsrc wq = make_rsrc((char*)a.dq + kbase, kspan), wk = make_rsrc((char*)a.dk + kbase, kspan);
 #pragma unroll
-  for (int b = 0; b < 2; ++b)
+  for (int b = 0; b < TB; ++b)
 #pragma unroll
     for (int i = 0; i < TQ; ++i) {
       const int nt = nq * TQ + i;
-      if (TN % 4 == 0 || nt < TN) {
-        const uint32_t off = (16 * (2 * tp + b) + r) * krow + (16 * nt + 4 * q) * ES;
+      if (FULL || nt < TN) {
+        const uint32_t off = (16 * (TB * tp + b) + r) * krow + (16 * nt + 4 * q) * ES;
         store4io(wq, off, dqs[b][i], IO{});
         store4io(wk, off, dks[b][i], IO{});
       }
@@ -409,15 +434,18 @@ __global__ __launch_bounds__(512) void delta_grads_kernel(DeltaArgs a) {
 
 hipError_t launch_delta_bwd_grads(const DeltaProb& p, const DeltaArgs& a, hipStream_t st) {
   if (p.nck == 0) return hipSuccess;
-  const dim3 grid((unsigned)(p.nck * p.G)), block(512);
-  auto pick_p = [&](auto n, auto io) {
-    constexpr int N = decltype(n)::value;
+  const dim3 grid((unsigned)(p.nck * p.G));
+  auto go = [&](auto n, auto pp, auto io) {
+    constexpr int N = decltype(n)::value, P = decltype(pp)::value;
     using IO = decltype(io);
+    hipLaunchKernelGGL((delta_grads_kernel<N, P, IO>), grid, dim3(512), 0, st, a);
+  };
+  auto pick_p = [&](auto n, auto io) {
     switch (p.P) {
-      case 16: hipLaunchKernelGGL((delta_grads_kernel<N, 16, IO>), grid, block, 0, st, a); break;
-      case 32: hipLaunchKernelGGL((delta_grads_kernel<N, 32, IO>), grid, block, 0, st, a); break;
-      case 64: hipLaunchKernelGGL((delta_grads_kernel<N, 64, IO>), grid, block, 0, st, a); break;
-      default: hipLaunchKernelGGL((delta_grads_kernel<N, 128, IO>), grid, block, 0, st, a); break;
+      case 16: go(n, std::integral_constant<int, 16>{}, io); break;
+      case 32: go(n, std::integral_constant<int, 32>{}, io); break;
+      case 64: go(n, std::integral_constant<int, 64>{}, io); break;
+      default: go(n, std::integral_constant<int, 128>{}, io); break;
     }
   };
   auto pick = [&](auto io) {
