@@ -99,7 +99,6 @@ __device__ __forceinline__ int row_at(int p, int t) {
   return (((p >> 4) * 4 + (t >> 5) * 2 + ((t >> 2) & 1)) * 64 + ((t & 31) >> 3) * 16 + (p & 15)) * 4 + (t & 3);
 }
 
-hipError_t launch_delta_f32_prep(const DeltaProb& p, const DeltaArgs& a, hipStream_t st);
 hipError_t launch_delta_f32_fwd(const DeltaProb& p, const DeltaArgs& a, hipStream_t st);
 hipError_t launch_delta_f32_bwd(const DeltaProb& p, const DeltaArgs& a, hipStream_t st);
 hipError_t launch_delta_prep(const DeltaProb& p, const DeltaArgs& a, hipStream_t st);
