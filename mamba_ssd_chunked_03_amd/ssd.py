@@ -159,8 +159,8 @@ def _dev(*ts):
         if not t.is_contiguous():
             raise ValueError("libssd needs contiguous tensors")
         if dev is None:
-            dev = t.device
-        elif t.device != dev:
+            dev, index = t.device, t.get_device()
+        elif t.get_device() != index:
             raise ValueError("all tensors must be on one device")
     return dev
 
@@ -172,6 +172,8 @@ def _expect(t, name, shape, dtype, required=True):
     if t is None:
         if required:
             raise ValueError("%s is required" % name)
+        return
+    if isinstance(t, torch.Tensor) and t.dtype == dtype and t.shape == shape:
         return
     if not isinstance(t, torch.Tensor):
         raise ValueError("%s must be a tensor" % name)
@@ -613,10 +615,18 @@ def _delta_problem(dims, packed, scale, flags=0):
 
 
 def _launcher(fn, args, dev, keep):
-    """launch(): the call, with `dev` current (a NULL stream is the current device's)."""
-    def launch():
-        with torch.cuda.device(dev):
-            _check(fn(*args), keep)
+    """launch(): the call, with `dev` current (a NULL stream is the current device's).
+    keep: objects the marshalled arguments point into."""
+    index = dev.index
+
+    def launch(keep=keep):
+        if torch.cuda.current_device() == index:
+            status = fn(*args)
+        else:
+            with torch.cuda.device(index):
+                status = fn(*args)
+        if status:
+            raise SSDError(status)
     return launch
 
 
