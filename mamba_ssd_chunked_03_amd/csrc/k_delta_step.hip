@@ -48,7 +48,8 @@ __device__ __forceinline__ float dot4(f32x4 a, f32x4 b) {
   return a[0] * b[0] + a[1] * b[1] + a[2] * b[2] + a[3] * b[3];
 }
 
-template <int N, class IO, int RPT>
+// RPT rows a thread, E groups of four columns of each (N / 4E lanes a row)
+template <int N, class IO, int RPT, int E>
 __global__ __launch_bounds__(256) void delta_step_kernel(int T, int H, int G, int P, float scale,
                                                          const typename IO::T* __restrict__ Q,
                                                          const typename IO::T* __restrict__ K,
@@ -56,7 +57,7 @@ __global__ __launch_bounds__(256) void delta_step_kernel(int T, int H, int G, in
                                                          const float* __restrict__ g, const float* __restrict__ beta,
                                                          const int32_t* __restrict__ slots, int nslots,
                                                          float* __restrict__ states, typename IO::T* __restrict__ out) {
-  constexpr int LPR = N / 4, RP = 256 / LPR;  // lanes a row, rows a pass
+  constexpr int LPR = N / (4 * E), RP = 256 / LPR, NC = N / E;  // lanes a row, rows a pass
   const int blocks = (P + RP * RPT - 1) / (RP * RPT);
   const int rb = blockIdx.x % blocks, h = (int)((blockIdx.x / blocks) % H), b = (int)(blockIdx.x / blocks / H);
   const int lr = threadIdx.x / LPR, n0 = (threadIdx.x % LPR) * 4;
@@ -64,15 +65,18 @@ __global__ __launch_bounds__(256) void delta_step_kernel(int T, int H, int G, in
   // a token's inputs, loaded while the one before is worked on (the first: beside the slots; the
   // state after them: before the slots' check it costs 10%, its reads then run ahead of the writes)
   const int grp = h / (H / G);
-  f32x4 k, q;
+  f32x4 k[E], q[E];
   float gt, bt, v[RPT];
   int p[RPT];
 #pragma unroll
   for (int i = 0; i < RPT; ++i) p[i] = rb * RP * RPT + i * RP + lr;
   auto load = [&](int t) {
     const int64_t tok = (int64_t)b * T + t;
-    k = io4(K + (tok * G + grp) * N + n0);
-    q = io4(Q + (tok * G + grp) * N + n0);
+#pragma unroll
+    for (int c = 0; c < E; ++c) {
+      k[c] = io4(K + (tok * G + grp) * N + c * NC + n0);
+      q[c] = io4(Q + (tok * G + grp) * N + c * NC + n0);
+    }
     gt = g[tok * H + h];
     bt = beta[tok * H + h];
 #pragma unroll
@@ -82,52 +86,72 @@ __global__ __launch_bounds__(256) void delta_step_kernel(int T, int H, int G, in
   load(0);
   if (slots && !slot_runs(slots, b, slot, nslots, mine)) return;  // (the same for the whole workgroup)
   float* S = states + ((int64_t)slot * H + h) * P * N;
-  f32x4 s[RPT];
+  f32x4 s[RPT][E];
 #pragma unroll
   for (int i = 0; i < RPT; ++i)
-    s[i] = p[i] < P ? __builtin_nontemporal_load((const f32x4*)(S + (int64_t)p[i] * N + n0)) : f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int c = 0; c < E; ++c)
+      s[i][c] = p[i] < P ? __builtin_nontemporal_load((const f32x4*)(S + (int64_t)p[i] * N + c * NC + n0))
+                         : f32x4{0.f, 0.f, 0.f, 0.f};
+  auto dot = [](const f32x4 (&x)[E], const f32x4 (&y)[E]) {
+    float d = dot4(x[0], y[0]);
+#pragma unroll
+    for (int c = 1; c < E; ++c) d += dot4(x[c], y[c]);
+    return row_total<LPR>(d);
+  };
   for (int t = 0; t < T; ++t) {
     const int64_t tok = (int64_t)b * T + t;
-    const f32x4 kt = k, qt = q;
-    const float a = expf(min_gate(gt)), b1 = bt;
+    f32x4 kt[E], qt[E];
     float vt[RPT];
 #pragma unroll
+    for (int c = 0; c < E; ++c) {
+      kt[c] = k[c];
+      qt[c] = q[c];
+    }
+#pragma unroll
     for (int i = 0; i < RPT; ++i) vt[i] = v[i];
+    const float a = expf(min_gate(gt)), b1 = bt;
     if (t + 1 < T) load(t + 1);
-    const float kq = row_total<LPR>(dot4(kt, qt));
+    const float kq = dot(kt, qt);
 #pragma unroll
     for (int i = 0; i < RPT; ++i) {
-      const float sk = row_total<LPR>(dot4(s[i], kt)), sq = row_total<LPR>(dot4(s[i], qt));
+      const float sk = dot(s[i], kt), sq = dot(s[i], qt);
       const float u = b1 * (vt[i] - a * sk);
 #pragma unroll
-      for (int e = 0; e < 4; ++e) s[i][e] = a * s[i][e] + u * kt[e];
+      for (int c = 0; c < E; ++c)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) s[i][c][e] = a * s[i][c][e] + u * kt[c][e];
       if (n0 == 0 && p[i] < P) put1(out + (tok * H + h) * P + p[i], scale * (a * sq + u * kq));
     }
   }
 #pragma unroll
   for (int i = 0; i < RPT; ++i)
-    if (p[i] < P) __builtin_nontemporal_store(s[i], (f32x4*)(S + (int64_t)p[i] * N + n0));
+#pragma unroll
+    for (int c = 0; c < E; ++c)
+      if (p[i] < P) __builtin_nontemporal_store(s[i][c], (f32x4*)(S + (int64_t)p[i] * N + c * NC + n0));
 }
 
 template <int N, class IO>
 static void step_go(const DeltaProb& p, const void* q, const void* k, const void* v, const float* g,
                     const float* beta, const int32_t* slots, int nslots, float* states, void* out, hipStream_t st) {
   using T = typename IO::T;
-  constexpr int RP = 256 / (N / 4);
-  auto go = [&](auto rpt, int64_t wgs) {
-    hipLaunchKernelGGL((delta_step_kernel<N, IO, decltype(rpt)::value>), dim3((unsigned)wgs), dim3(256), 0, st, p.L, p.H,
-                       p.G, p.P, p.scale, (const T*)q, (const T*)k, (const T*)v, g, beta, slots, nslots, states,
-                       (T*)out);
+  constexpr int E = N >= 64 ? 2 : 1;
+  auto go = [&](auto rpt, auto e, int64_t wgs) {
+    hipLaunchKernelGGL((delta_step_kernel<N, IO, decltype(rpt)::value, decltype(e)::value>), dim3((unsigned)wgs),
+                       dim3(256), 0, st, p.L, p.H, p.G, p.P, p.scale, (const T*)q, (const T*)k, (const T*)v, g, beta,
+                       slots, nslots, states, (T*)out);
   };
-  auto count = [&](int rpt) { return (int64_t)p.B * p.H * ((p.P + RP * rpt - 1) / (RP * rpt)); };
-  // Rows a thread.  Several tokens: four, which share a token's loads, k . q and gate (5 tokens,
-  // 24 sequences of 32 heads of 128 x 128: 32 us, two rows 36), unless they leave CUs without
-  // work.  One token: two (250 sequences of 64 heads of 64 x 128: one row 289 us, two 188,
-  // four 202, eight 199; one sequence: 3.7, 3.9, 5.3, 5.6).
-  if (p.L > 1 && count(4) >= 1024)
-    go(std::integral_constant<int, 4>{}, count(4));
+  auto count = [&](int rows) { return (int64_t)p.B * p.H * ((p.P + rows - 1) / rows); };
+  constexpr int R1 = 2 * 1024 / N, R2 = 4 * 1024 / N;  // rows a workgroup: two or four groups of four columns a thread
+  // Several tokens: four groups of four columns a thread, which share a token's loads, k . q and
+  // gate, at dstate 64 and more as two rows of two, whose sums take fewer lanes (5 tokens, 24
+  // sequences of 32 heads of 128 x 128: 30 us, four rows of one 32, two 36), unless they leave
+  // CUs without work.  One token: two rows (250 sequences of 64 heads of 64 x 128: one 289 us,
+  // two 188, four 202, eight 199; one sequence: 3.7, 3.9, 5.3, 5.6).
+  if (p.L > 1 && count(R2) >= 1024)
+    go(std::integral_constant<int, 4 / E>{}, std::integral_constant<int, E>{}, count(R2));
   else
-    go(std::integral_constant<int, 2>{}, count(2));
+    go(std::integral_constant<int, 2>{}, std::integral_constant<int, 1>{}, count(R1));
 }
 
 hipError_t launch_delta_step(const DeltaProb& p, const void* q, const void* k, const void* v, const float* g,

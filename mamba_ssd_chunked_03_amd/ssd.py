@@ -230,7 +230,13 @@ def problem(x, B, cu_seqlens=None, dt_softplus=True, flags=0):
                    int(flags))
 
 
+# (without the Stream object between, 2 us less a call)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
 def _stream(dev):
+    if _raw_stream is not None:
+        return ctypes.c_void_p(_raw_stream(dev.index))
     return ctypes.c_void_p(torch.cuda.current_stream(dev).cuda_stream)
 
 
