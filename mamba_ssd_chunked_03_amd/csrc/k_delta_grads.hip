@@ -309,11 +309,12 @@ __global__ __launch_bounds__(512) void delta_grads_kernel(DeltaArgs a) {
       if (J <= I) {
         const float Gh = gl[tok], Gl = gl[C + tok];
         const f32x4 jh = *(const f32x4*)(gl + 16 * J + 4 * q), jl = *(const f32x4*)(gl + C + 16 * J + 4 * q);
+        const int last = tok - md - (16 * J + 4 * q);  // (dP with its diagonal, dM without)
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          const int j = 16 * J + 4 * q + e;
-          const float d = exp2_fast((Gh - jh[e]) + (Gl - jl[e]));
-          v[e] = (md == 0 ? j <= tok : j < tok) ? f * (cc[i][e] * d) : 0.f;
+          float x = f * (cc[i][e] * exp2_fast((Gh - jh[e]) + (Gl - jl[e])));
+          asm("" : "+v"(x));  // (formed in any case: no branch an element)
+          v[e] = e <= last ? x : 0.f;
         }
       }
       uint2 o[PM];
@@ -330,12 +331,13 @@ __global__ __launch_bounds__(512) void delta_grads_kernel(DeltaArgs a) {
     const int q2 = l2 >> 4, r2 = l2 & 15;
     // k and q of a tile's token and columns (planes add up to the input exactly)
     auto value = [&](const uint16_t* X, int tok, int nt) {
-      f32x4 v = zero;
-#pragma unroll
-      for (int m = PI - 1; m >= 0; --m) {
+      auto plane = [&](int m) {
         const uint2 x = *(const uint2*)(X + m * KPL + tok * LN + 16 * nt + 4 * q2);
-        v += f32x4{bf_lo(x.x), bf_hi(x.x), bf_lo(x.y), bf_hi(x.y)};
-      }
+        return f32x4{bf_lo(x.x), bf_hi(x.x), bf_lo(x.y), bf_hi(x.y)};
+      };
+      f32x4 v = plane(PI - 1);
+#pragma unroll
+      for (int m = PI - 2; m >= 0; --m) v += plane(m);
       return v;
     };
     float dwr[TB];  // this lane's part of w
