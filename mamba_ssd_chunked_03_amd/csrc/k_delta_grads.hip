@@ -66,6 +66,7 @@ __global__ __launch_bounds__(512) void delta_grads_kernel(DeltaArgs a) {
   ChunkInfo ci = chunk_info(a.map, ck);
   const int start = __builtin_amdgcn_readfirstlane(ci.start), len = __builtin_amdgcn_readfirstlane(ci.len);
   if (len <= 0) return;
+  const bool bare = ci.first && !a.init;
   const uint32_t krow = (uint32_t)a.G * N * ES, kspan = (uint32_t)(len - 1) * krow + N * ES;
   const int64_t kbase = ((int64_t)start * a.G + grp) * N * ES;
   const brsrc rk = make_rsrc((const char*)a.k + kbase, kspan), rq = make_rsrc((const char*)a.q + kbase, kspan);
@@ -163,7 +164,8 @@ __global__ __launch_bounds__(512) void delta_grads_kernel(DeltaArgs a) {
     x = __shfl(x, rl);
     if (lane < len) {
       const int64_t at = ((int64_t)start + lane) * a.H + grp * per + hh;
-      a.dg[at] = x + y;
+      // (a gate with no state to decay: what is left of the sums there is their rounding)
+      a.dg[at] = bare && lane == 0 ? 0.f * (x + y) : x + y;
       a.dbeta[at] = db;
     }
   };

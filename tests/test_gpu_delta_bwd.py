@@ -209,3 +209,17 @@ def test_layer_run_with_the_gated_norm():
     ref = oracle_bwd(dict(d, dout=torch.from_numpy(rdy).view(1, 150, 8, 64)))
     for n in NAMES:
         assert rel(f64(g[n]), ref[n]) <= OUT_TOL["bf16"] + 1e-2 + TOL["bf16"][n], n
+
+
+@pytest.mark.parametrize("io", ["bf16", "f32"])
+def test_first_gates_without_a_state_have_no_gradient(io):
+    """A sequence's first gate decays its initial state alone: without one its gradient is zero,
+    not what rounding leaves of sums that cancel."""
+    lengths = [1, 70, 1, 0, 130]
+    d = make(1, sum(lengths), 4, 2, 32, 64, io=io, lengths=lengths, init=False, seed=11)
+    c = cuda(d)
+    got = ssd.delta_bwd(c["q"], c["k"], c["v"], c["g"], c["beta"], c["dout"], scale=d["scale"], cu_seqlens=c["cu"],
+                        d_final=c["d_final"])
+    first = [0, 1, 71, 72]
+    assert (got["dg"][0, first] == 0).all()
+    assert (got["dg"][0, 2:71].abs().amax(0) > 0).all()
