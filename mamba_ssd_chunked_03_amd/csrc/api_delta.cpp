@@ -92,8 +92,8 @@ DeltaLayout delta_layout(const DeltaProb& p) {
   return l;
 }
 
-// Point the chunk map at the table in the workspace and queue its build (SSD_DEBUG=1:
-// after checking cu_seqlens on the host).
+// Point the chunk map at the table in the workspace and, unless a forward kept it there,
+// queue its build (SSD_DEBUG=1: after checking cu_seqlens on the host).
 ssd_status setup_map(DeltaProb& p, const DeltaLayout& l, const int32_t* cu, char* ws, hipStream_t st) {
   if (!p.packed) return SSD_OK;
   p.map.tab = (const int4*)(ws + l.tab);
@@ -109,6 +109,7 @@ ssd_status setup_map(DeltaProb& p, const DeltaLayout& l, const int32_t* cu, char
     for (int s = 0; s < p.nst; ++s)
       if (hcu[s + 1] < hcu[s]) return SSD_ERR_VARLEN;
   }
+  if (p.flags & SSD_FLAG_FROM_SAVED) return SSD_OK;
   Prob t;
   std::memset(&t, 0, sizeof(t));
   t.nseq = p.nst;

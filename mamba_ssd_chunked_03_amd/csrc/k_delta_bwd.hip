@@ -5,7 +5,7 @@
 //   E = P^T dO + exp(G_C - G) K dS^T          (adjoint of U)
 //   F = E - (b R)^T E,   dX = b F = dV         (adjoints of U in full, and of X)
 //   dS <- exp(G_C) dS + (scale exp(G) dO)^T Q - (exp(G) dX)^T K
-// F and the dS of every chunk are stored for k_delta_grads.hip, which forms the gradients
+// F and the planes of every chunk's dS are stored for k_delta_grads.hip, which forms the gradients
 // chunk by chunk.  Registers, waves and tiles as in k_delta_fwd.hip.  The helper waves form
 // what does not wait for dS a chunk ahead: E0 = P^T dO and T = (scale exp(G) dO)^T Q.
 //   interval A(c)  chain: K dS^T, E                 helpers: T(c), Q, P, dO(c - 1) to LDS
@@ -29,12 +29,11 @@ __global__ __launch_bounds__(64 * NPT * kSplit<N> + 256, 1) void delta_bwd_kerne
   __shared__ __align__(16) f32x4 Kx[SPLIT == 2 ? NPT : 1][SPLIT][4][64];  // parts of K dS^T
 
   const int tid = threadIdx.x, w = __builtin_amdgcn_readfirstlane(tid >> 6), lane = tid & 63, q = lane >> 4, r = lane & 15;
-  const int np = (ptiles + NPT - 1) / NPT;
+  const int np = ptiles / NPT;
   int s, wg;
   chain_order(a.H * np, s, wg);
   const int pg = wg % np, h = wg / np;
   const int p0 = pg * 16 * NPT;
-  const int pw = 16 * min(NPT, ptiles - pg * NPT);
   const int grp = h / (a.H / a.G);
   const SeqSpan sp = seq_span(a.map, s);
   const int c0 = sp.c0, c1 = sp.c1;
@@ -43,7 +42,6 @@ __global__ __launch_bounds__(64 * NPT * kSplit<N> + 256, 1) void delta_bwd_kerne
   if (w < CW) {
     // ------------------------------------------------------------ chain wave ----
     const int tw = w / SPLIT, half = w % SPLIT, kb = half * KH;
-    const bool live = 16 * tw < pw;
     const int pc = p0 + 16 * tw + r;
     f32x4 S[KH][2];  // columns 32(kb + k) + 8q + 4t + e of row pc
     const int64_t srow = (((int64_t)s * a.H + h) * a.P + pc) * N;
@@ -52,8 +50,8 @@ __global__ __launch_bounds__(64 * NPT * kSplit<N> + 256, 1) void delta_bwd_kerne
     for (int k = 0; k < KH; ++k)
 #pragma unroll
       for (int t = 0; t < 2; ++t)
-        S[k][t] = a.d_final && live && scol(k, t) < N ? *(const f32x4*)(a.d_final + srow + scol(k, t)) : zero;
-    f32x4* kS = (f32x4*)a.dS + (int64_t)(pc >> 4) * (KS * 2) * 64 + lane;  // of chunk slot 0
+        S[k][t] = a.d_final && scol(k, t) < N ? *(const f32x4*)(a.d_final + srow + scol(k, t)) : zero;
+    u32x4* kS = (u32x4*)a.dS + (int64_t)(pc >> 4) * (KS * 2) * 64 + lane;  // of chunk slot 0
     f32x4* kF = (f32x4*)a.F + (int64_t)(pc >> 4) * 4 * 64 + lane;
     __syncthreads();
     __syncthreads();
@@ -85,9 +83,9 @@ __global__ __launch_bounds__(64 * NPT * kSplit<N> + 256, 1) void delta_bwd_kerne
 #pragma unroll
             for (int i = 0; i < 4; ++i) ks[i] = mfma_bf16(kf[k][i], sf[k].p[m], ks[i]);
           if (k + 1 < KH) sf[k + 1] = tile_planes<2>(S[k + 1][0], S[k + 1][1]);
-          if (live)
 #pragma unroll
-            for (int t = 0; t < 2; ++t) kS[(kh * (a.P / 16) * (KS * 2) + (kb + k) * 2 + t) * 64] = S[k][t];
+          for (int m = 0; m < 2; ++m)
+            kS[(kh * (a.P / 16) * (KS * 2) + (kb + k) * 2 + m) * 64] = __builtin_bit_cast(u32x4, sf[k].p[m]);
           if (k + 1 == KH) {
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
@@ -145,7 +143,7 @@ __global__ __launch_bounds__(64 * NPT * kSplit<N> + 256, 1) void delta_bwd_kerne
           for (int t = 0; t < 2; ++t) {
             const int i = 2 * B + t;
             F[i] = E[i] - F[i];
-            if (live && B == half) kF[(kh * (a.P / 16) * 4 + i) * 64] = F[i];
+            if (B == half) kF[(kh * (a.P / 16) * 4 + i) * 64] = F[i];
             wv[t] = -(wg4[i] * F[i]);
           }
           wf[B] = tile_planes<2>(wv[0], wv[1]);
@@ -211,9 +209,9 @@ __global__ __launch_bounds__(64 * NPT * kSplit<N> + 256, 1) void delta_bwd_kerne
 #pragma unroll
             for (int t = 0; t < 2; ++t) ks[2 + t] = mfma_bf16(kf[k][t], sf[k].p[m], ks[2 + t]);
           if (k + 1 < KS) sf[k + 1] = tile_planes<2>(S[k + 1][0], S[k + 1][1]);
-          if (live)
 #pragma unroll
-            for (int t = 0; t < 2; ++t) kS[(kh * (a.P / 16) * (KS * 2) + k * 2 + t) * 64] = S[k][t];
+          for (int m = 0; m < 2; ++m)
+            kS[(kh * (a.P / 16) * (KS * 2) + k * 2 + m) * 64] = __builtin_bit_cast(u32x4, sf[k].p[m]);
           interleave<4, 4>();
           __builtin_amdgcn_sched_barrier(0);
         }
@@ -276,7 +274,7 @@ __global__ __launch_bounds__(64 * NPT * kSplit<N> + 256, 1) void delta_bwd_kerne
           for (int t = 0; t < 2; ++t) {
             const int i = 2 * B + t;
             F[i] = E[i] - F[i];
-            if (live) kF[(kh * (a.P / 16) * 4 + i) * 64] = F[i];
+            kF[(kh * (a.P / 16) * 4 + i) * 64] = F[i];
             wv[t] = -(wg4[i] * F[i]);
           }
           wf[B] = tile_planes<2>(wv[0], wv[1]);
@@ -298,7 +296,7 @@ __global__ __launch_bounds__(64 * NPT * kSplit<N> + 256, 1) void delta_bwd_kerne
         __syncthreads();
       }
     }
-    if (a.d_init && live) {
+    if (a.d_init) {
 #pragma unroll
       for (int k = 0; k < KH; ++k)
 #pragma unroll
@@ -312,7 +310,7 @@ __global__ __launch_bounds__(64 * NPT * kSplit<N> + 256, 1) void delta_bwd_kerne
   // (of a tile: HT blocks of 16 tokens of E0 and TK blocks of 32 columns of T a wave)
   constexpr int HT = NPT, TK = KS * NPT < 4 ? 1 : KS * NPT / 4;
   const int ht = tid - 64 * CW, tile = (w - CW) % NPT, i0 = (w - CW) / NPT * HT, k0 = (w - CW) / NPT * TK;
-  const bool works = 16 * tile < pw, sums = works && k0 < KS;
+  const bool sums = k0 < KS;
   if constexpr (N < 32) {
     for (int e = ht; e < C; e += 256)
       for (int c = N; c < 32; c += 4) {
@@ -355,11 +353,11 @@ __global__ __launch_bounds__(64 * NPT * kSplit<N> + 256, 1) void delta_bwd_kerne
     const int start = sp.start + (c - c0) * C, len = min(C, sp.end - start);
     const uint32_t vrow = (uint32_t)a.H * a.P * 2;
     const brsrc ro = make_rsrc((const char*)a.dout + (((int64_t)start * a.H + h) * a.P + p0) * 2,
-                               (uint32_t)(len - 1) * vrow + pw * 2);
+                               (uint32_t)(len - 1) * vrow + 32 * NPT);
 #pragma unroll
     for (int i = 0; i < VC; ++i) {
       const int e = ht + i * 256;
-      xo[i] = buf_load16(ro, (VX || e < C * VP) && 8 * (e % VP) < pw ? (e / VP) * vrow + (e % VP) * 16 : kNoOffset);
+      xo[i] = buf_load16(ro, VX || e < C * VP ? (e / VP) * vrow + (e % VP) * 16 : kNoOffset);
     }
     const int64_t kh = (int64_t)c * a.H + h;
     const brsrc rp = make_rsrc(a.Pt + kh * ER, ER * 2);
@@ -397,7 +395,6 @@ __global__ __launch_bounds__(64 * NPT * kSplit<N> + 256, 1) void delta_bwd_kerne
   f32x4 T[TK][2];
   // E0 (to LDS) and T (kept) of the chunk in Pl, Ol, Ql
   auto ahead = [&](int buf) {
-    if (!works) return;
     const float* g = gl[buf];
     Planes<2> Pf[HT][2], df[2];
     bf16x8 of[2];
@@ -502,7 +499,7 @@ hipError_t launch_delta_bwd_chain(const DeltaProb& p, const DeltaArgs& a, hipStr
   const int64_t heads = (int64_t)p.nst * p.H;
   auto go = [&](auto n, auto npt) {
     constexpr int N = decltype(n)::value, NPT = decltype(npt)::value;
-    hipLaunchKernelGGL((delta_bwd_kernel<N, NPT>), dim3((unsigned)(heads * ((ptiles + NPT - 1) / NPT))),
+    hipLaunchKernelGGL((delta_bwd_kernel<N, NPT>), dim3((unsigned)(heads * (ptiles / NPT))),
                        dim3(64 * NPT * kSplit<N> + 256), 0, st, a, ptiles);
   };
   auto pick = [&](auto n) {

@@ -50,12 +50,11 @@ __global__ __launch_bounds__(64 * NPT * kSplit<N> + 256, 1) void delta_fwd_kerne
   __shared__ __align__(16) f32x4 Kx[SPLIT == 2 ? NPT : 1][SPLIT][4][64];  // parts of K S^T
 
   const int tid = threadIdx.x, w = __builtin_amdgcn_readfirstlane(tid >> 6), lane = tid & 63, q = lane >> 4, r = lane & 15;
-  const int np = (ptiles + NPT - 1) / NPT;
+  const int np = ptiles / NPT;
   int s, wg;
   chain_order(a.H * np, s, wg);
   const int pg = wg % np, h = wg / np;
   const int p0 = pg * 16 * NPT;                      // the workgroup's columns
-  const int pw = 16 * min(NPT, ptiles - pg * NPT);   // (a last workgroup may have fewer)
   const int grp = h / (a.H / a.G);
   const SeqSpan sp = seq_span(a.map, s);
   const int c0 = sp.c0, c1 = sp.c1;
@@ -64,7 +63,6 @@ __global__ __launch_bounds__(64 * NPT * kSplit<N> + 256, 1) void delta_fwd_kerne
   if (w < CW) {
     // ------------------------------------------------------------ chain wave ----
     const int tw = w / SPLIT, half = w % SPLIT, kb = half * KH;
-    const bool live = 16 * tw < pw;
     const int pc = p0 + 16 * tw + r;  // this lane's column of headdim
     // the state: S[k][t] holds columns 32(kb + k) + 8q + 4t + e of row pc
     f32x4 S[KH][2];
@@ -74,8 +72,8 @@ __global__ __launch_bounds__(64 * NPT * kSplit<N> + 256, 1) void delta_fwd_kerne
     for (int k = 0; k < KH; ++k)
 #pragma unroll
       for (int t = 0; t < 2; ++t)
-        S[k][t] = a.init && live && scol(k, t) < N ? *(const f32x4*)(a.init + srow + scol(k, t)) : zero;
-    f32x4* kS = (f32x4*)a.S + (int64_t)(pc >> 4) * (KS * 2) * 64 + lane;  // of chunk slot 0 (SAVE)
+        S[k][t] = a.init && scol(k, t) < N ? *(const f32x4*)(a.init + srow + scol(k, t)) : zero;
+    u32x4* kS = (u32x4*)a.S + (int64_t)(pc >> 4) * (KS * 2) * 64 + lane;  // of chunk slot 0 (SAVE)
     f32x4* kZ = (f32x4*)a.Z + (int64_t)(pc >> 4) * 4 * 64 + lane;
     __syncthreads();
     if constexpr (SPLIT == 2) {
@@ -109,9 +107,9 @@ __global__ __launch_bounds__(64 * NPT * kSplit<N> + 256, 1) void delta_fwd_kerne
 #pragma unroll
           for (int m = 0; m < 2; ++m) Sx[tw][kb + k][m][lane] = __builtin_bit_cast(u32x4, sf[k].p[m]);
           if constexpr (SAVE)
-            if (live)
 #pragma unroll
-              for (int t = 0; t < 2; ++t) kS[(kh * (a.P / 16) * (KS * 2) + (kb + k) * 2 + t) * 64] = S[k][t];
+            for (int m = 0; m < 2; ++m)
+              kS[(kh * (a.P / 16) * (KS * 2) + (kb + k) * 2 + m) * 64] = __builtin_bit_cast(u32x4, sf[k].p[m]);
           if (k + 1 == KH) {
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
@@ -174,7 +172,7 @@ __global__ __launch_bounds__(64 * NPT * kSplit<N> + 256, 1) void delta_fwd_kerne
             if (B == half) {
               Zx[tw][i][lane] = Z[i];
               if constexpr (SAVE)
-                if (live) kZ[(kh * (a.P / 16) * 4 + i) * 64] = Z[i];
+                kZ[(kh * (a.P / 16) * 4 + i) * 64] = Z[i];
             }
           }
           wf[B] = tile_planes<3>(wg4[2 * B] * Z[2 * B], wg4[2 * B + 1] * Z[2 * B + 1]);
@@ -245,9 +243,9 @@ __global__ __launch_bounds__(64 * NPT * kSplit<N> + 256, 1) void delta_fwd_kerne
 #pragma unroll
           for (int m = 0; m < 2; ++m) Sx[w][k][m][lane] = __builtin_bit_cast(u32x4, sf[k].p[m]);
           if constexpr (SAVE)
-            if (live)
 #pragma unroll
-              for (int t = 0; t < 2; ++t) kS[(kh * (a.P / 16) * (KS * 2) + k * 2 + t) * 64] = S[k][t];
+            for (int m = 0; m < 2; ++m)
+              kS[(kh * (a.P / 16) * (KS * 2) + k * 2 + m) * 64] = __builtin_bit_cast(u32x4, sf[k].p[m]);
           interleave<4, 4>();
           __builtin_amdgcn_sched_barrier(0);
         }
@@ -315,7 +313,7 @@ __global__ __launch_bounds__(64 * NPT * kSplit<N> + 256, 1) void delta_fwd_kerne
             Z[i] = X[i] - Z[i];
             Zx[w][i][lane] = Z[i];
             if constexpr (SAVE)
-              if (live) kZ[(kh * (a.P / 16) * 4 + i) * 64] = Z[i];
+              kZ[(kh * (a.P / 16) * 4 + i) * 64] = Z[i];
           }
           wf[B] = tile_planes<3>(wg4[2 * B] * Z[2 * B], wg4[2 * B + 1] * Z[2 * B + 1]);
         };
@@ -338,7 +336,7 @@ __global__ __launch_bounds__(64 * NPT * kSplit<N> + 256, 1) void delta_fwd_kerne
       }
     }
     __syncthreads();
-    if (a.final_states && live) {
+    if (a.final_states) {
 #pragma unroll
       for (int k = 0; k < KH; ++k)
 #pragma unroll
@@ -352,7 +350,7 @@ __global__ __launch_bounds__(64 * NPT * kSplit<N> + 256, 1) void delta_fwd_kerne
   // (the outputs of a tile: HT blocks of 16 tokens a wave)
   constexpr int HT = NPT;
   const int ht = tid - 64 * CW, tile = (w - CW) % NPT, i0 = (w - CW) / NPT * HT;
-  const bool outs = a.out && 16 * tile < pw;  // (no output where a backward recomputes)
+  const bool outs = a.out;  // (no output where a backward recomputes)
   if constexpr (N < 32) {  // the products' depth is 32: columns past N are zero
     for (int e = ht; e < C; e += 256)
       for (int c = N; c < 32; c += 4) {
@@ -391,11 +389,11 @@ __global__ __launch_bounds__(64 * NPT * kSplit<N> + 256, 1) void delta_fwd_kerne
     const int start = sp.start + (c - c0) * C, len = min(C, sp.end - start);
     const uint32_t vrow = (uint32_t)a.H * a.P * 2;
     const brsrc rv = make_rsrc((const char*)a.v + (((int64_t)start * a.H + h) * a.P + p0) * 2,
-                               (uint32_t)(len - 1) * vrow + pw * 2);
+                               (uint32_t)(len - 1) * vrow + 32 * NPT);
 #pragma unroll
     for (int i = 0; i < VC; ++i) {
       const int e = ht + i * 256;
-      xv[i] = buf_load16(rv, (VX || e < C * VP) && 8 * (e % VP) < pw ? (e / VP) * vrow + (e % VP) * 16 : kNoOffset);
+      xv[i] = buf_load16(rv, VX || e < C * VP ? (e / VP) * vrow + (e % VP) * 16 : kNoOffset);
     }
     const int64_t kh = (int64_t)c * a.H + h;
     const brsrc rr = make_rsrc(a.R + kh * ER, ER * 2);
@@ -468,7 +466,7 @@ __global__ __launch_bounds__(64 * NPT * kSplit<N> + 256, 1) void delta_fwd_kerne
     const int start = sp.start + (c - c0) * C, len = min(C, sp.end - start);
     const uint32_t vrow = (uint32_t)a.H * a.P * 2;
     const brsrc ro = make_rsrc((char*)a.out + (((int64_t)start * a.H + h) * a.P + p0) * 2,
-                               (uint32_t)(len - 1) * vrow + pw * 2);
+                               (uint32_t)(len - 1) * vrow + 32 * NPT);
 #pragma unroll
     for (int ii = 0; ii < HT; ++ii)
       store4io(ro, (32 * ((i0 + ii) >> 1) + row32(r, (i0 + ii) & 1)) * vrow + (16 * tile + 4 * q) * 2, qs[ii], IoBf16{});
@@ -537,7 +535,7 @@ hipError_t launch_delta_fwd(const DeltaProb& p, const DeltaArgs& a, hipStream_t 
   auto go = [&](auto n, auto npt, auto save) {
     constexpr int N = decltype(n)::value, NPT = decltype(npt)::value;
     hipLaunchKernelGGL((delta_fwd_kernel<N, NPT, decltype(save)::value>),
-                       dim3((unsigned)(heads * ((ptiles + NPT - 1) / NPT))), dim3(64 * NPT * kSplit<N> + 256), 0, st, a,
+                       dim3((unsigned)(heads * (ptiles / NPT))), dim3(64 * NPT * kSplit<N> + 256), 0, st, a,
                        ptiles);
   };
   auto pick_npt = [&](auto n, auto save) {
