@@ -437,8 +437,9 @@ ssd_status ssd_gated_rmsnorm_bwd(const ssd_norm_problem* problem, const void* do
  *  - g below -256 counts as -256 (exp of it is zero in fp32): a gate of -inf resets the
  *    state.  beta = 0 writes nothing; its own gradient is still the formula's.
  *  - Chunked form (ssd_delta_fwd, ssd_delta_bwd): chunks of 64 tokens.  The states and
- *    the gradients of g, beta and init are fp32 results of fp32 accuracy (operands of
- *    the matrix products are split into two bf16 parts, three for fp32 io).  An
+ *    the gradients of g, beta and init are fp32 results (operands of the matrix
+ *    products are split into two bf16 parts, three in the state's update and with fp32
+ *    io: with bf16 io they are off by a few 2^-18 of their terms).  An
  *    infinity or a NaN in an input can spread over its whole chunk, earlier tokens of
  *    it included, and goes on through the states; later sequences are not touched.
  *  - Tokens behind the last sequence of cu_seqlens are not computed: their rows of
