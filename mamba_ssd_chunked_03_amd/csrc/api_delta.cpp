@@ -64,6 +64,12 @@ ssd_status make_delta(const ssd_delta_problem* pr, int packed, DeltaProb& p) {
   return SSD_OK;
 }
 
+// Whether the gradients take a workgroup a head, and the heads' dq and dk are added up after (in
+// the same order: the bits do not change).  Backward calls from a saved forward, dstate 128, us
+// with a group's heads in one workgroup | apart: 16 chunks and groups of 8 heads 79 | 39, 64 of 8
+// 91 | 68, 128 of 4 64 | 68, 128 of 8 114 | 125, 512 of 4 184 | 266.
+bool split_heads(const DeltaProb& p) { return p.G < p.H && p.nck * p.G <= 64; }
+
 DeltaLayout delta_layout(const DeltaProb& p) {
   DeltaLayout l;
   std::memset(&l, 0, sizeof(l));
@@ -88,6 +94,7 @@ DeltaLayout delta_layout(const DeltaProb& p) {
   l.Z = take(ch * rows);
   l.dS = take(ch * state);
   l.F = take(ch * rows);
+  l.parts = take(split_heads(p) ? ch * 2 * kDeltaChunk * p.N * 4 : 0);
   l.end = o;
   return l;
 }
@@ -238,6 +245,7 @@ ssd_status ssd_delta_bwd(const ssd_delta_problem* pr, const void* q, const void*
   a.F = (float*)(ws + l.F);
   a.d_init = d_init_states;
   a.dq = dq; a.dk = dk; a.dv = dv; a.dg = dg; a.dbeta = dbeta;
+  a.parts = split_heads(p) ? (float*)(ws + l.parts) : nullptr;
   DELTA_TRY(launch_delta_bwd_chain(p, a, st));
   DELTA_TRY(launch_delta_bwd_grads(p, a, st));
   return SSD_OK;

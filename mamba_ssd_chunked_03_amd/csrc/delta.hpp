@@ -56,7 +56,7 @@ struct DeltaProb {
 // Regions of the workspace (byte offsets, 256-byte aligned).
 struct DeltaLayout {
   size_t tab, seq_off, gates, R, Pm, fwd_end;  // the forward's
-  size_t Rt, Pt, S, Z, dS, F, end;             // kept for the backward, and the backward's
+  size_t Rt, Pt, S, Z, dS, F, parts, end;      // kept for the backward, and the backward's
 };
 
 // Per-problem pointers of the chunked kernels.
@@ -78,6 +78,7 @@ struct DeltaArgs {
   float* d_init;
   void *dq, *dk, *dv;
   float *dg, *dbeta;
+  float* parts;                // (nck, H, 2, 64, dstate): each head's dq and dk, or null: summed in one workgroup
 };
 
 // Per (chunk, head), 64 tokens each: running log2 decay G (high part, low part), beta; and

@@ -13,15 +13,18 @@
 // w_j enters dg_i as the sum over j < i and exp(G_C) <S, dS> alone is carried, instead of
 // two large sums that cancel.  dg is the suffix sum of dL/dG within the chunk.
 //
-// dq and dk are summed over the group's heads in registers, in order.  Eight waves: wave w
+// dq and dk are summed over the group's heads in registers, in order (of few chunks and groups, a
+// workgroup takes one head, and delta_head_sum_kernel adds them up).  Eight waves: wave w
 // has tokens 32 (w % 2)..+31 and a quarter (w / 2) of the N columns, which reads each
 // operand from LDS two to four times (16 tokens and half the columns a wave: 1.3 times as
 // much; sixteen waves, 1.5 times as much, 925 us below), and three of the 24 blocks of dP and
 // dM that are formed (16 rows a wave: 5% more).  The running sums of a head's gates are formed
 // by one wave while the others begin the next head.
-// 2 x 8192 tokens, 64 heads in 8 groups, 64 x 128: 720 us, 11 a head, of which a workgroup's
-// matrix instructions take 1.7, vector ones 3.5, and LDS 5 with its conflicts: phases between
-// barriers, two waves a SIMD, with the next head's loads in flight (2.6 TB/s).
+// 2 x 8192 tokens, 64 heads in 8 groups, 64 x 128: 726 us, 11 a head, of which a workgroup's
+// matrix instructions take 1.7, vector ones 3.2, and LDS 5 with its conflicts: phases between
+// barriers, two waves a SIMD, with the next head's loads in flight (2.6 TB/s).  (LDS rows
+// exchanged by an exclusive or instead of padded: a third of the conflicts, 12% more vector
+// instructions, the same time.)
 #include "delta.hpp"
 
 namespace ssd {
@@ -62,7 +65,9 @@ __global__ __launch_bounds__(512) void delta_grads_kernel(DeltaArgs a) {
     return b < 12;
   };
   const int wg = xcd_order(blockIdx.x, gridDim.x);
-  const int ck = wg / a.G, grp = wg % a.G, per = a.H / a.G;
+  // heads h0..h1-1 of group grp: all of them, or one (their sums then follow in a kernel of its own)
+  const int per = a.H / a.G, nh = a.parts ? a.H : a.G, ck = wg / nh, grp = a.parts ? wg % nh / per : wg % nh;
+  const int h0 = a.parts ? wg % nh : grp * per, h1 = a.parts ? h0 + 1 : h0 + per;
   ChunkInfo ci = chunk_info(a.map, ck);
   const int start = __builtin_amdgcn_readfirstlane(ci.start), len = __builtin_amdgcn_readfirstlane(ci.len);
   if (len <= 0) return;
@@ -112,7 +117,7 @@ __global__ __launch_bounds__(512) void delta_grads_kernel(DeltaArgs a) {
   Raw8<IO> xo;
   float xg;
   auto load_s = [&](int hh, int pb) {
-    const int64_t kh = (int64_t)ck * a.H + grp * per + hh;
+    const int64_t kh = (int64_t)ck * a.H + hh;
     int td = tid;
     asm("" : "+v"(td));
     const brsrc rs = make_rsrc(a.S + kh * P * NP, P * NP * 4), rd = make_rsrc(a.dS + kh * P * NP, P * NP * 4);
@@ -126,7 +131,7 @@ __global__ __launch_bounds__(512) void delta_grads_kernel(DeltaArgs a) {
     }
   };
   auto load = [&](int hh, int pb) {
-    const int h = grp * per + hh;
+    const int h = hh;
     const int64_t kh = (int64_t)ck * a.H + h;
     int td = tid;  // (not seen to be the same: the offsets are formed anew)
     asm("" : "+v"(td));
@@ -172,18 +177,18 @@ __global__ __launch_bounds__(512) void delta_grads_kernel(DeltaArgs a) {
     const float y = wave_inclusive_sum(wj) - wj;
     x = __shfl(x, rl);
     if (lane < len) {
-      const int64_t at = ((int64_t)start + lane) * a.H + grp * per + hh;
+      const int64_t at = ((int64_t)start + lane) * a.H + hh;
       // (a gate with no state to decay: what is left of the sums there is their rounding)
       a.dg[at] = bare && lane == 0 ? 0.f * (x + y) : x + y;
       a.dbeta[at] = db;
     }
   };
 
-  load_s(0, 0);
-  load(0, 0);
+  load_s(h0, 0);
+  load(h0, 0);
 #pragma unroll 1
-  for (int hh = 0; hh < per; ++hh) {
-    const int h = grp * per + hh;
+  for (int hh = h0; hh < h1; ++hh) {
+    const int h = hh;
     const brsrc rdv = make_rsrc((char*)a.dv + ((int64_t)start * a.H + h) * P * ES, (uint32_t)(len - 1) * vrow + P * ES);
     f32x4 dq[TB][TQ], dr[TB][TQ], dw[TB][TQ], cc[CB];
 #pragma unroll
@@ -258,9 +263,9 @@ __global__ __launch_bounds__(512) void delta_grads_kernel(DeltaArgs a) {
         for (int m = 0; m < PI; ++m) *(u32x4*)(Ol + m * OPL + td / (PB / 8) * LP + (td % (PB / 8)) * 8) = o[m];
       }
       if (tid < 3 * C) gl[tid] = xg;
-      if (pb == 0 && hh > 0 && w == hh % NW) gates(hh - 1);
+      if (pb == 0 && hh > h0 && w == hh % NW) gates(hh - 1);
       if constexpr (NB > 1) {
-        const int it = min(hh * NB + pb + 1, per * NB - 1);
+        const int it = min(hh * NB + pb + 1, h1 * NB - 1);
         load(it / NB, it % NB);
       }
       __syncthreads();
@@ -314,7 +319,7 @@ __global__ __launch_bounds__(512) void delta_grads_kernel(DeltaArgs a) {
         }
       }
       if constexpr (NB > 1) {
-        const int it = min(hh * NB + pb + 1, per * NB - 1);
+        const int it = min(hh * NB + pb + 1, h1 * NB - 1);
         load_s(it / NB, it % NB);
       }
       __syncthreads();
@@ -359,7 +364,7 @@ __global__ __launch_bounds__(512) void delta_grads_kernel(DeltaArgs a) {
     if constexpr (!KEEP) put_kq();
     __syncthreads();
     // (one block of headdim: the next head's loads, where the registers of the first part are free)
-    if constexpr (NB == 1) load(min(hh + 1, per - 1), 0);
+    if constexpr (NB == 1) load(min(hh + 1, h1 - 1), 0);
     int l2 = lane;
     asm("" : "+v"(l2));
     const int q2 = l2 >> 4, r2 = l2 & 15;
@@ -418,7 +423,7 @@ __global__ __launch_bounds__(512) void delta_grads_kernel(DeltaArgs a) {
         }
         __builtin_amdgcn_sched_barrier(0);
       }
-    if constexpr (NB == 1) load_s(min(hh + 1, per - 1), 0);
+    if constexpr (NB == 1) load_s(min(hh + 1, h1 - 1), 0);
     __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
     for (int b = 0; b < TB; ++b) {
@@ -453,7 +458,21 @@ __global__ __launch_bounds__(512) void delta_grads_kernel(DeltaArgs a) {
     }
     __syncthreads();  // (the next head's data goes where P and M are)
   }
-  if (w == 0) gates(per - 1);
+  if (w == 0) gates(h1 - 1);
+  if (a.parts) {
+    float* part = a.parts + ((int64_t)ck * a.H + h0) * 2 * C * N;
+#pragma unroll
+    for (int b = 0; b < TB; ++b)
+#pragma unroll
+      for (int i = 0; i < TQ; ++i) {
+        const int nt = nq * TQ + i, at = (16 * (TB * tp + b) + r) * N + 16 * nt + 4 * q;
+        if (FULL || nt < TN) {
+          *(f32x4*)(part + at) = dqs[b][i];
+          *(f32x4*)(part + C * N + at) = dks[b][i];
+        }
+      }
+    return;
+  }
   const brsrc wq = make_rsrc((char*)a.dq + kbase, kspan), wk = make_rsrc((char*)a.dk + kbase, kspan);
 #pragma unroll
   for (int b = 0; b < TB; ++b)
@@ -468,9 +487,33 @@ __global__ __launch_bounds__(512) void delta_grads_kernel(DeltaArgs a) {
     }
 }
 
+// dq and dk of a chunk and group from its heads' parts, added in the order of the heads (the sums
+// are those of a workgroup that takes all of them).
+template <int N, class IO>
+__global__ __launch_bounds__(256) void delta_head_sum_kernel(DeltaArgs a) {
+  constexpr int C = kDeltaChunk, ES = sizeof(typename IO::T), ROWS = 1024 / N;
+  const int blk = blockIdx.x % (C / ROWS), wg = blockIdx.x / (C / ROWS);
+  const int ck = wg / a.G, grp = wg % a.G, per = a.H / a.G;
+  const ChunkInfo ci = chunk_info(a.map, ck);
+  const int tok = blk * ROWS + threadIdx.x / (N / 4), col = threadIdx.x % (N / 4) * 4;
+  if (tok >= ci.len) return;
+  const float* p = a.parts + (((int64_t)ck * a.H + grp * per) * 2 * C + tok) * N + col;
+  f32x4 dq = {0.f, 0.f, 0.f, 0.f}, dk = dq;
+  for (int h = 0; h < per; ++h, p += 2 * C * N) {
+    dq += *(const f32x4*)p;
+    dk += *(const f32x4*)(p + C * N);
+  }
+  const int start = __builtin_amdgcn_readfirstlane(ci.start), len = __builtin_amdgcn_readfirstlane(ci.len);
+  const uint32_t row = (uint32_t)a.G * N * ES;
+  const int64_t at = ((int64_t)start * a.G + grp) * N * ES;
+  const uint32_t span = (uint32_t)(len - 1) * row + N * ES;
+  store4io(make_rsrc((char*)a.dq + at, span), tok * row + col * ES, dq, IO{});
+  store4io(make_rsrc((char*)a.dk + at, span), tok * row + col * ES, dk, IO{});
+}
+
 hipError_t launch_delta_bwd_grads(const DeltaProb& p, const DeltaArgs& a, hipStream_t st) {
   if (p.nck == 0) return hipSuccess;
-  const dim3 grid((unsigned)(p.nck * p.G));
+  const dim3 grid((unsigned)(p.nck * (a.parts ? p.H : p.G)));
   auto go = [&](auto n, auto pp, auto io) {
     constexpr int N = decltype(n)::value, P = decltype(pp)::value;
     using IO = decltype(io);
@@ -493,6 +536,21 @@ hipError_t launch_delta_bwd_grads(const DeltaProb& p, const DeltaArgs& a, hipStr
     }
   };
   p.io ? pick(IoBf16{}) : pick(IoF32{});
+  if (!a.parts) return hipGetLastError();
+  auto sum = [&](auto n, auto io) {
+    constexpr int N = decltype(n)::value;
+    hipLaunchKernelGGL((delta_head_sum_kernel<N, decltype(io)>), dim3((unsigned)(p.nck * p.G * (kDeltaChunk * N / 1024))),
+                       dim3(256), 0, st, a);
+  };
+  auto pick_sum = [&](auto io) {
+    switch (p.N) {
+      case 16: sum(std::integral_constant<int, 16>{}, io); break;
+      case 32: sum(std::integral_constant<int, 32>{}, io); break;
+      case 64: sum(std::integral_constant<int, 64>{}, io); break;
+      default: sum(std::integral_constant<int, 128>{}, io); break;
+    }
+  };
+  p.io ? pick_sum(IoBf16{}) : pick_sum(IoF32{});
   return hipGetLastError();
 }
 

@@ -223,3 +223,17 @@ def test_first_gates_without_a_state_have_no_gradient(io):
     first = [0, 1, 71, 72]
     assert (got["dg"][0, first] == 0).all()
     assert (got["dg"][0, 2:71].abs().amax(0) > 0).all()
+
+
+@pytest.mark.parametrize("io", ["bf16", "f32"])
+def test_gradients_of_many_sequences_are_those_of_each(io):
+    """Few chunks and groups give each head a workgroup, many do not: the same bits."""
+    B = 26
+    d = make(B, 130, 6, 2, 32, 64, io=io, seed=12)
+    c = cuda(d)
+    whole = run_bwd(d)
+    for b in (0, 7, B - 1):
+        one = ssd.delta_bwd(*(x[b:b + 1] for x in args(c)), c["dout"][b:b + 1], scale=d["scale"],
+                            init=c["init"][b:b + 1], d_final=c["d_final"][b:b + 1])
+        for n in NAMES:
+            assert torch.equal(one[n], whole[n][b:b + 1]), (b, n)
