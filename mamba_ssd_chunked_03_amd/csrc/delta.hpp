@@ -86,13 +86,12 @@ struct DeltaArgs {
 // end G stays and beta is zero.
 constexpr int kDeltaGates = 7 * kDeltaChunk;
 
-// States and their adjoints per (chunk, head), and Z and F, are kept in the order of the
-// chains' tiles, 16 columns of headdim after the other, so that a wave stores 1 KB runs;
-// NP = dstate or 32.  States with fp32 io: fp32 (P / 16, NP / 32, 2, 64 lanes, 4), lane 16 q + r
-// of tile (k, t) holding row r, columns 32k + 8q + 4t + 0..3; with bf16 io the two planes that
-// the chains' products and the gradients take (P / 16, NP / 32, 2 planes, 64 lanes, 8 bf16), lane
-// 16 q + r of block k row r, columns 32k + 8q + 0..7.  Z, F: fp32 (P / 16, 4, 64 lanes, 4), lane
-// 16 q + r of tile i column r of tokens 32 (i / 2) + 8q + 4 (i % 2) + 0..3.
+// States and their adjoints per (chunk, head), and Z and F, are kept in fp32 in the order of the
+// chains' accumulator tiles, 16 columns of headdim after the other, so that a wave stores
+// 1 KB runs: states (P / 16, NP / 32, 2, 64 lanes, 4), NP = dstate or 32, lane 16 q + r of
+// tile (k, t) holding row r, columns 32k + 8q + 4t + 0..3; Z, F (P / 16, 4, 64 lanes, 4),
+// lane 16 q + r of tile i column r of tokens 32 (i / 2) + 8q + 4 (i % 2) + 0..3.  (As the two planes
+// that the products take, <S, dS> would lose three digits: 4e-5 of dg over a few tokens.)
 __host__ __device__ __forceinline__ int state_cols(int N) { return N < 32 ? 32 : N; }
 // float offset of columns n..n+3 (n a multiple of 4) of headdim row p
 __device__ __forceinline__ int state_at(int p, int n, int NP) {

@@ -5,7 +5,7 @@
 //   E = P^T dO + exp(G_C - G) K dS^T          (adjoint of U)
 //   F = E - (b R)^T E,   dX = b F = dV         (adjoints of U in full, and of X)
 //   dS <- exp(G_C) dS + (scale exp(G) dO)^T Q - (exp(G) dX)^T K
-// F and the planes of every chunk's dS are stored for k_delta_grads.hip, which forms the gradients
+// F and the dS of every chunk are stored for k_delta_grads.hip, which forms the gradients
 // chunk by chunk.  Registers, waves and tiles as in k_delta_fwd.hip.  The helper waves form
 // what does not wait for dS a chunk ahead: E0 = P^T dO and T = (scale exp(G) dO)^T Q.
 //   interval A(c)  chain: K dS^T, E                 helpers: T(c), Q, P, dO(c - 1) to LDS
@@ -51,7 +51,7 @@ __global__ __launch_bounds__(64 * NPT * kSplit<N> + 256, 1) void delta_bwd_kerne
 #pragma unroll
       for (int t = 0; t < 2; ++t)
         S[k][t] = a.d_final && scol(k, t) < N ? *(const f32x4*)(a.d_final + srow + scol(k, t)) : zero;
-    u32x4* kS = (u32x4*)a.dS + (int64_t)(pc >> 4) * (KS * 2) * 64 + lane;  // of chunk slot 0
+    f32x4* kS = (f32x4*)a.dS + (int64_t)(pc >> 4) * (KS * 2) * 64 + lane;  // of chunk slot 0
     f32x4* kF = (f32x4*)a.F + (int64_t)(pc >> 4) * 4 * 64 + lane;
     __syncthreads();
     __syncthreads();
@@ -84,8 +84,7 @@ __global__ __launch_bounds__(64 * NPT * kSplit<N> + 256, 1) void delta_bwd_kerne
             for (int i = 0; i < 4; ++i) ks[i] = mfma_bf16(kf[k][i], sf[k].p[m], ks[i]);
           if (k + 1 < KH) sf[k + 1] = tile_planes<2>(S[k + 1][0], S[k + 1][1]);
 #pragma unroll
-          for (int m = 0; m < 2; ++m)
-            kS[(kh * (a.P / 16) * (KS * 2) + (kb + k) * 2 + m) * 64] = __builtin_bit_cast(u32x4, sf[k].p[m]);
+          for (int t = 0; t < 2; ++t) kS[(kh * (a.P / 16) * (KS * 2) + (kb + k) * 2 + t) * 64] = S[k][t];
           if (k + 1 == KH) {
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
@@ -210,8 +209,7 @@ __global__ __launch_bounds__(64 * NPT * kSplit<N> + 256, 1) void delta_bwd_kerne
             for (int t = 0; t < 2; ++t) ks[2 + t] = mfma_bf16(kf[k][t], sf[k].p[m], ks[2 + t]);
           if (k + 1 < KS) sf[k + 1] = tile_planes<2>(S[k + 1][0], S[k + 1][1]);
 #pragma unroll
-          for (int m = 0; m < 2; ++m)
-            kS[(kh * (a.P / 16) * (KS * 2) + k * 2 + m) * 64] = __builtin_bit_cast(u32x4, sf[k].p[m]);
+          for (int t = 0; t < 2; ++t) kS[(kh * (a.P / 16) * (KS * 2) + k * 2 + t) * 64] = S[k][t];
           interleave<4, 4>();
           __builtin_amdgcn_sched_barrier(0);
         }

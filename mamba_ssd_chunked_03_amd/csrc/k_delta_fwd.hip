@@ -73,7 +73,7 @@ __global__ __launch_bounds__(64 * NPT * kSplit<N> + 256, 1) void delta_fwd_kerne
 #pragma unroll
       for (int t = 0; t < 2; ++t)
         S[k][t] = a.init && scol(k, t) < N ? *(const f32x4*)(a.init + srow + scol(k, t)) : zero;
-    u32x4* kS = (u32x4*)a.S + (int64_t)(pc >> 4) * (KS * 2) * 64 + lane;  // of chunk slot 0 (SAVE)
+    f32x4* kS = (f32x4*)a.S + (int64_t)(pc >> 4) * (KS * 2) * 64 + lane;  // of chunk slot 0 (SAVE)
     f32x4* kZ = (f32x4*)a.Z + (int64_t)(pc >> 4) * 4 * 64 + lane;
     __syncthreads();
     if constexpr (SPLIT == 2) {
@@ -108,8 +108,7 @@ __global__ __launch_bounds__(64 * NPT * kSplit<N> + 256, 1) void delta_fwd_kerne
           for (int m = 0; m < 2; ++m) Sx[tw][kb + k][m][lane] = __builtin_bit_cast(u32x4, sf[k].p[m]);
           if constexpr (SAVE)
 #pragma unroll
-            for (int m = 0; m < 2; ++m)
-              kS[(kh * (a.P / 16) * (KS * 2) + (kb + k) * 2 + m) * 64] = __builtin_bit_cast(u32x4, sf[k].p[m]);
+            for (int t = 0; t < 2; ++t) kS[(kh * (a.P / 16) * (KS * 2) + (kb + k) * 2 + t) * 64] = S[k][t];
           if (k + 1 == KH) {
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
@@ -244,8 +243,7 @@ __global__ __launch_bounds__(64 * NPT * kSplit<N> + 256, 1) void delta_fwd_kerne
           for (int m = 0; m < 2; ++m) Sx[w][k][m][lane] = __builtin_bit_cast(u32x4, sf[k].p[m]);
           if constexpr (SAVE)
 #pragma unroll
-            for (int m = 0; m < 2; ++m)
-              kS[(kh * (a.P / 16) * (KS * 2) + k * 2 + m) * 64] = __builtin_bit_cast(u32x4, sf[k].p[m]);
+            for (int t = 0; t < 2; ++t) kS[(kh * (a.P / 16) * (KS * 2) + k * 2 + t) * 64] = S[k][t];
           interleave<4, 4>();
           __builtin_amdgcn_sched_barrier(0);
         }

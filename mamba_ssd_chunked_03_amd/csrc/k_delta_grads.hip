@@ -20,8 +20,8 @@
 // much; sixteen waves, 1.5 times as much, 925 us below), and three of the 24 blocks of dP and
 // dM that are formed (16 rows a wave: 5% more).  The running sums of a head's gates are formed
 // by one wave while the others begin the next head.
-// 2 x 8192 tokens, 64 heads in 8 groups, 64 x 128: 726 us, 11 a head, of which a workgroup's
-// matrix instructions take 1.7, vector ones 3.2, and LDS 5 with its conflicts: phases between
+// 2 x 8192 tokens, 64 heads in 8 groups, 64 x 128: 737 us, 11 a head, of which a workgroup's
+// matrix instructions take 1.7, vector ones 3.5, and LDS 5 with its conflicts: phases between
 // barriers, two waves a SIMD, with the next head's loads in flight (2.6 TB/s).  (LDS rows
 // exchanged by an exclusive or instead of padded: a third of the conflicts, 12% more vector
 // instructions, the same time.)
@@ -100,17 +100,10 @@ __global__ __launch_bounds__(512) void delta_grads_kernel(DeltaArgs a) {
   // into registers while the one before is worked on, all through range-checked resources
   // (past headdim they are zero).
   constexpr int SE = PB * NP / 4, RE = PB * C / 4, OE = C * PB / 8;
-  constexpr int SP = SE / 128, SC = KEEP ? 2 * ((SP + NW - 1) / NW) : (SE + NTH - 1) / NTH, RC = (RE + NTH - 1) / NTH, TPR = NP / 16;
+  constexpr int SC = (SE + NTH - 1) / NTH, RC = (RE + NTH - 1) / NTH, TPR = NP / 16;
   static_assert(OE <= NTH && 3 * C <= NTH && RE % NTH == 0 && NW % TPR == 0, "pieces of a thread");
-  // bf16 io: the chains keep two planes of the states, in their operands' order: wave w's pieces
-  // 2i + m are plane m of rows 16 x.., columns 32 y + 8q.. where KS x + y = i NW + w.  fp32 io: fp32,
-  // piece i rows 16 (i NW / TPR + w / TPR).., column tile w % TPR.  Of Z and F: rows 16 (i NW / 4 +
-  // w / 4).., token tile w % 4
-  constexpr int KS = NP / 32;
-  auto has = [&](int i, int qq) {  // a piece of the states
-    return KEEP ? (SP % NW == 0 || (i >> 1) * NW + w < SP) && (N == NP || 8 * qq < N)
-                : (SE % NTH == 0 || i * NTH + tid < SE) && (N == NP || 32 * ((w % TPR) >> 1) + 8 * qq + 4 * (w & 1) < N);
-  };
+  // wave w's tile i of the states: rows 16 (i NW / TPR + w / TPR).., column tile w % TPR; of Z
+  // and F: rows 16 (i NW / 4 + w / 4).., token tile w % 4
   const int tk4 = 32 * ((w & 3) >> 1) + 8 * q + 4 * (w & 1);  // (the same tokens in each)
   const int scol = 32 * ((w % TPR) >> 1) + 8 * q + 4 * (w & 1);
   u32x4 xs[SC], xd[SC], xz[RC], xf_[RC], xb;
@@ -123,11 +116,9 @@ __global__ __launch_bounds__(512) void delta_grads_kernel(DeltaArgs a) {
     const brsrc rs = make_rsrc(a.S + kh * P * NP, P * NP * 4), rd = make_rsrc(a.dS + kh * P * NP, P * NP * 4);
 #pragma unroll
     for (int i = 0; i < SC; ++i) {
-      const uint32_t at = KEEP ? (td >> 6) * 2048 + (td & 63) * 16 : td * 16;
-      const int step = KEEP ? (i >> 1) * NW * 2048 + (i & 1) * 1024 : i * NTH * 16;
-      const uint32_t off = has(i, (td & 63) >> 4) ? at : kNoOffset;
-      xs[i] = buf_load16(rs, off, pb * SE * 16 + step);
-      xd[i] = buf_load16(rd, off, pb * SE * 16 + step);
+      const uint32_t off = (SE % NTH == 0 || td + i * NTH < SE) && (N == NP || scol < N) ? td * 16 : kNoOffset;
+      xs[i] = buf_load16(rs, off, (pb * SE + i * NTH) * 16);
+      xd[i] = buf_load16(rd, off, (pb * SE + i * NTH) * 16);
     }
   };
   auto load = [&](int hh, int pb) {
@@ -204,42 +195,19 @@ __global__ __launch_bounds__(512) void delta_grads_kernel(DeltaArgs a) {
       int td = tid;
       asm("" : "+v"(td));
       const int lr = td & 15;
-      if constexpr (KEEP) {
 #pragma unroll
-        for (int i = 0; i < SC; i += 2) {
-          const int x = (i >> 1) * NW + w, at = (16 * (x / KS) + lr) * LN + 32 * (x % KS) + 8 * q;
+      for (int i = 0; i < SC; ++i) {
+        const int at = (16 * (i * (NW / TPR) + w / TPR) + lr) * LN + scol;
+        const f32x4 x = __builtin_bit_cast(f32x4, xs[i]), y = __builtin_bit_cast(f32x4, xd[i]);
+        sdot += x[0] * y[0] + x[1] * y[1] + x[2] * y[2] + x[3] * y[3];
+        if ((SE % NTH == 0 || td + i * NTH < SE) && (N == NP || scol < N)) {
+          uint2 o[PM];
+          split4<PM>(x, o);
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {  // <S, dS>, by planes
-            // (a bit_cast of a vector's element itself takes the first one's bits)
-            const uint32_t s0w = xs[i][e], s1w = xs[i + 1][e], d0w = xd[i][e], d1w = xd[i + 1][e];
-            const bf16x2v s0 = __builtin_bit_cast(bf16x2v, s0w), s1 = __builtin_bit_cast(bf16x2v, s1w);
-            const bf16x2v d0 = __builtin_bit_cast(bf16x2v, d0w), d1 = __builtin_bit_cast(bf16x2v, d1w);
-            sdot = __builtin_amdgcn_fdot2_f32_bf16(s1, d0, sdot, false);
-            sdot = __builtin_amdgcn_fdot2_f32_bf16(s0, d1, sdot, false);
-            sdot = __builtin_amdgcn_fdot2_f32_bf16(s0, d0, sdot, false);
-          }
-          if (has(i, q))
+          for (int m = 0; m < PM; ++m) *(uint2*)(Sl + m * SPL + at) = o[m];
+          split4<PM>(y, o);
 #pragma unroll
-            for (int m = 0; m < 2; ++m) {
-              *(u32x4*)(Sl + m * SPL + at) = xs[i + m];
-              *(u32x4*)(Dl + m * SPL + at) = xd[i + m];
-            }
-        }
-      } else {
-#pragma unroll
-        for (int i = 0; i < SC; ++i) {
-          const int at = (16 * (i * (NW / TPR) + w / TPR) + lr) * LN + 32 * ((w % TPR) >> 1) + 8 * q + 4 * (w & 1);
-          const f32x4 x = __builtin_bit_cast(f32x4, xs[i]), y = __builtin_bit_cast(f32x4, xd[i]);
-          sdot += x[0] * y[0] + x[1] * y[1] + x[2] * y[2] + x[3] * y[3];
-          if (has(i, q)) {
-            uint2 o[PM];
-            split4<PM>(x, o);
-#pragma unroll
-            for (int m = 0; m < PM; ++m) *(uint2*)(Sl + m * SPL + at) = o[m];
-            split4<PM>(y, o);
-#pragma unroll
-            for (int m = 0; m < PM; ++m) *(uint2*)(Dl + m * SPL + at) = o[m];
-          }
+          for (int m = 0; m < PM; ++m) *(uint2*)(Dl + m * SPL + at) = o[m];
         }
       }
       const f32x4 b = __builtin_bit_cast(f32x4, xb);

@@ -237,3 +237,17 @@ def test_gradients_of_many_sequences_are_those_of_each(io):
                             init=c["init"][b:b + 1], d_final=c["d_final"][b:b + 1])
         for n in NAMES:
             assert torch.equal(one[n], whole[n][b:b + 1]), (b, n)
+
+
+@pytest.mark.parametrize("io", ["bf16", "f32"])
+def test_gates_of_a_few_tokens(io):
+    """dg of short sequences with an initial state, sums that can cancel: the error is held against
+    the terms' absolute values, of which <|init|, |d_final|> for every token is a part.  A product
+    is off by at most 3 x 2^-18 of its terms with bf16 io (two planes an operand), by 2^-26 and
+    fp32 sums of at most 128 + 64 terms (2^-20 together) with fp32 io; <S, dS> by fp32 rounding."""
+    lengths = [1, 2, 3, 1, 4]
+    d = make(1, sum(lengths), 2, 1, 32, 32, io=io, lengths=lengths, seed=21)
+    got, ref = f64(run_bwd(d)["dg"]), oracle_bwd(d)["dg"]
+    init, dfin = f64(d["init"]), f64(d["d_final"])
+    terms = np.sqrt(sum(l * (np.abs(init[s]) * np.abs(dfin[s])).sum((-1, -2)) ** 2 for s, l in enumerate(lengths)).sum())
+    assert np.linalg.norm(got - ref) <= (3 * 2.0 ** -18 if io == "bf16" else 2.0 ** -20) * terms
