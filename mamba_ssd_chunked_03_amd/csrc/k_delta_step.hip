@@ -142,12 +142,18 @@ static void step_go(const DeltaProb& p, const void* q, const void* k, const void
                        slots, nslots, states, (T*)out);
   };
   auto count = [&](int rows) { return (int64_t)p.B * p.H * ((p.P + rows - 1) / rows); };
-  constexpr int R1 = 2 * 1024 / N, R2 = 4 * 1024 / N;  // rows a workgroup: two or four groups of four columns a thread
-  // Several tokens: four groups of four columns a thread, which share a token's loads, k . q and
-  // gate, at dstate 64 and more as two rows of two, whose sums take fewer lanes (5 tokens, 24
-  // sequences of 32 heads of 128 x 128: 30 us, four rows of one 32, two 36), unless they leave
-  // CUs without work.  One token: two rows (250 sequences of 64 heads of 64 x 128: one 289 us,
+  // rows a workgroup: two, four or eight groups of four columns a thread
+  constexpr int R1 = 2 * 1024 / N, R2 = 4 * 1024 / N, R3 = 8 * 1024 / N;
+  // Several tokens: more groups a thread, which share a token's loads, k . q and gate, dealt to few
+  // rows, whose sums then take fewer lanes, while they fill the CUs.  5 tokens, 24 sequences of 32
+  // heads of 128 x 128, us by rows a thread x groups: 1 x 2 36, 2 x 1 36, 4 x 1 32, 2 x 2 29, 1 x 4
+  // 34, 4 x 2 26, 2 x 4 25.  One token: two rows (250 sequences of 64 heads of 64 x 128: one 289 us,
   // two 188, four 202, eight 199; one sequence: 3.7, 3.9, 5.3, 5.6).
+  if constexpr (N >= 64)
+    if (p.L > 1 && p.P % R3 == 0 && count(R3) >= 1024) {
+      go(std::integral_constant<int, 2>{}, std::integral_constant<int, 4>{}, count(R3));
+      return;
+    }
   if (p.L > 1 && count(R2) >= 1024)
     go(std::integral_constant<int, 4 / E>{}, std::integral_constant<int, E>{}, count(R2));
   else

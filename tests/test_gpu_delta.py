@@ -324,3 +324,24 @@ def test_a_nan_gate_is_not_dropped(io, dims):
     assert torch.isnan(o1[1, 0, 2].float()).all() and torch.isnan(s1[1, 2]).all()
     o1[1, 0, 2], s1[1, 2] = o0[1, 0, 2], s0[1, 2]
     assert torch.equal(o0, o1) and torch.equal(s0, s1)
+
+
+@pytest.mark.parametrize("heads,groups,headdim,dstate,io", [
+    (16, 4, 64, 128, "bf16"), (8, 8, 128, 64, "bf16"), (8, 2, 64, 64, "f32"), (16, 4, 32, 128, "bf16"),
+    (16, 16, 128, 32, "bf16"), (16, 1, 64, 16, "f32")])
+def test_drafted_tokens_of_a_large_batch_are_the_single_ones(heads, groups, headdim, dstate, io):
+    """Enough sequences for the forms with more rows and columns a thread: three tokens in one call
+    against three calls.  Each is off by at most 1.2e-6 a token (see above): 7.2e-6 together, of
+    the states and, one rounding to bf16 on either side (2^-8 together), of the outputs."""
+    B, T = 136, 3
+    d = make(B, T, heads, groups, headdim, dstate, io=io, seed=headdim + dstate)
+    slots = torch.randperm(B + 3, generator=torch.Generator().manual_seed(1))[:B].to(torch.int32).cuda()
+    states = torch.randn(B + 3, heads, headdim, dstate, device="cuda")
+    one, c = states.clone(), cuda(d)
+    out = run_step(d, states, slots)
+    outs = [ssd.delta_step(*(c[n][:, t:t + 1].contiguous() for n in ("q", "k", "v", "g", "beta")), one, slots=slots,
+                           scale=d["scale"]) for t in range(T)]
+    assert rel(f64(states), f64(one)) <= 7.2e-6
+    assert rel(f64(out), f64(torch.cat(outs, 1))) <= (2.0 ** -8 if io == "bf16" else 7.2e-6)
+    unused = [i for i in range(B + 3) if i not in set(slots.tolist())]
+    assert torch.equal(states[unused], one[unused])

@@ -251,3 +251,22 @@ def test_gates_of_a_few_tokens(io):
     init, dfin = f64(d["init"]), f64(d["d_final"])
     terms = np.sqrt(sum(l * (np.abs(init[s]) * np.abs(dfin[s])).sum((-1, -2)) ** 2 for s, l in enumerate(lengths)).sum())
     assert np.linalg.norm(got - ref) <= (3 * 2.0 ** -18 if io == "bf16" else 2.0 ** -20) * terms
+
+
+@pytest.mark.parametrize("sizes", [(24, 130, 16, 4, 64, 128), (40, 70, 32, 4, 128, 64), (30, 200, 12, 4, 32, 16)], ids=str)
+def test_large_batches_are_their_sequences(sizes):
+    """Two tiles of headdim a workgroup of the chains, several heads a wave of the chunk matrices
+    (a group's three or four, and two) and a group's heads in one workgroup of the gradients
+    give the bits of the forms that one sequence takes."""
+    d = make(*sizes, io="bf16", seed=sum(sizes))
+    c = cuda(d)
+    ws = torch.empty(ssd.delta_workspace_bytes(c["k"], c["v"], backward=True), dtype=torch.uint8, device="cuda")
+    out, final = ssd.delta_fwd(*args(c), scale=d["scale"], init=c["init"], workspace=ws, save_for_backward=True)
+    whole = run_bwd(d, workspace=ws, from_saved=True)
+    for b in (0, sizes[0] // 2, sizes[0] - 1):
+        a, init, dfin = [x[b:b + 1] for x in args(c)], c["init"][b:b + 1], c["d_final"][b:b + 1]
+        o1, f1 = ssd.delta_fwd(*a, scale=d["scale"], init=init)
+        one = ssd.delta_bwd(*a, c["dout"][b:b + 1], scale=d["scale"], init=init, d_final=dfin)
+        assert torch.equal(out[b:b + 1], o1) and torch.equal(final[b:b + 1], f1)
+        for n in NAMES:
+            assert torch.equal(one[n], whole[n][b:b + 1]), (b, n)
